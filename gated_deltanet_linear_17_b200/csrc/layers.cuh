@@ -1,0 +1,92 @@
+// Device helpers shared by the kernels of gdn_layers.h: 8-element accesses of the three
+// activation types, and division by a run-time constant.
+#pragma once
+
+#include "common.cuh"
+#include "layers.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- 8 elements at a time
+// (16 bytes of a 16-bit type, 32 of fp32; the address is 16-byte aligned)
+struct Bf16 {
+    using raw = uint16_t;
+    static __device__ __forceinline__ float up(uint16_t x) { return bf2f(x); }
+    static __device__ __forceinline__ uint16_t down(float x) { return f2bf(x); }
+    static __device__ __forceinline__ float2 up2(uint32_t w) { return unpack2<false>(w); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b) { return pack_bf2(a, b); }
+};
+struct F16 {
+    using raw = uint16_t;
+    static __device__ __forceinline__ float up(uint16_t x) { return __half2float(__ushort_as_half(x)); }
+    static __device__ __forceinline__ uint16_t down(float x) { return __half_as_ushort(__float2half_rn(x)); }
+    static __device__ __forceinline__ float2 up2(uint32_t w) { return unpack_h2(w); }
+    static __device__ __forceinline__ uint32_t down2(float a, float b) { return pack_h2(a, b); }
+};
+struct F32 {
+    using raw = float;
+    static __device__ __forceinline__ float up(float x) { return x; }
+    static __device__ __forceinline__ float down(float x) { return x; }
+};
+
+// the 8 elements as they lie in memory
+template <class A>
+struct Raw8 {
+    uint4 w;
+    __device__ __forceinline__ void load(const typename A::raw *p) { w = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void store(typename A::raw *p) const { *reinterpret_cast<uint4 *>(p) = w; }
+    __device__ __forceinline__ void up(float (&x)[8]) const
+    {
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = A::up2(v[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+    }
+    __device__ __forceinline__ void down(const float (&x)[8])
+    {
+        w = make_uint4(A::down2(x[0], x[1]), A::down2(x[2], x[3]), A::down2(x[4], x[5]), A::down2(x[6], x[7]));
+    }
+};
+template <>
+struct Raw8<F32> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void store(float *p) const
+    {
+        reinterpret_cast<float4 *>(p)[0] = a;
+        reinterpret_cast<float4 *>(p)[1] = b;
+    }
+    __device__ __forceinline__ void up(float (&x)[8]) const
+    {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ __forceinline__ void down(const float (&x)[8])
+    {
+        a = make_float4(x[0], x[1], x[2], x[3]);
+        b = make_float4(x[4], x[5], x[6], x[7]);
+    }
+};
+
+// four floats -> four e4m3 bytes (nearest, halves to even, beyond 448 to 448, NaN kept), lowest byte first
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d)
+{
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+    return (uint32_t)hi << 16 | lo;
+}
+__device__ __forceinline__ uint8_t to_e4m3(float a) { return (uint8_t)(pack_e4m3(a, 0.f, 0.f, 0.f) & 0xff); }
+
+__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv d)
+{
+    return d.shift < 0 ? n : (uint32_t)(((uint64_t)n * d.mul) >> 32 >> d.shift);
+}
+
+}  // namespace gdn
