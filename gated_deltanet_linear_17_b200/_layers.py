@@ -48,6 +48,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _need(t, name, dtype, shape, dev):
+    """``_binding._need``, with the comparisons of a good tensor kept cheap (a decode step's calls are short)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
+        _b._need(t, name, dtype, shape, dev)
+
+
 @contextlib.contextmanager
 def _on(dev, stream):
     with torch.cuda.device(dev):
@@ -74,8 +81,10 @@ class _Here:
 
 
 def _place(dev, stream):
+    """Context of a call on ``dev``: the handle of the stream that it runs on, with torch's current stream set to it."""
     if stream is None and dev.index == torch.cuda.current_device():
-        return _Here(torch.cuda.current_stream().cuda_stream)
+        # the handle itself, a tenth of a microsecond against three for a Stream object
+        return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
     return _on(dev, stream)
 
 
@@ -112,34 +121,34 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
         raise ValueError("x must be [..., width] with at least one column")
     shape, dev = x.shape, x.device
     width = shape[-1]
-    _b._need(x, "x", act, shape, dev)
+    _need(x, "x", act, shape, dev)
     _cuda(weight, "weight")
     wdt = torch.float32 if weight.dtype == torch.float32 else act
-    _b._need(weight, "weight", wdt, (width,), dev)
+    _need(weight, "weight", wdt, (width,), dev)
     if residual is not None:
-        _b._need(residual, "residual", act, shape, dev)
+        _need(residual, "residual", act, shape, dev)
     if gate is not None:
-        _b._need(gate, "gate", act, shape, dev)
+        _need(gate, "gate", act, shape, dev)
     if residual_out is not None:
         if residual is None:
             raise ValueError("residual_out needs a residual")
-        _b._need(residual_out, "residual_out", act, shape, dev)
+        _need(residual_out, "residual_out", act, shape, dev)
     odt = act if quant is None else torch.float8_e4m3fn
     if out is not None:
-        _b._need(out, "out", odt, shape, dev)
+        _need(out, "out", odt, shape, dev)
     lead = shape[:-1]
     sshape = None if quant is None else lead if quant == "row" else (*lead, -(-width // QUANT_GROUP))
     if scales is not None:
         if quant is None:
             raise ValueError("scales need quant")
-        _b._need(scales, "scales", torch.float32, sshape, dev)
+        _need(scales, "scales", torch.float32, sshape, dev)
     with _place(dev, stream) as st:
         if out is None:
-            out = torch.empty(shape, dtype=odt, device=dev)
+            out = torch.empty_like(x) if quant is None else torch.empty_like(x, dtype=odt)
         if residual is not None and residual_out is None:
-            residual_out = torch.empty(shape, dtype=act, device=dev)
+            residual_out = torch.empty_like(x)
         if quant is not None and scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=dev)
+            scales = x.new_empty(sshape, dtype=torch.float32)
         rc = _layers_lib().gdn_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), float(eps),
                                         float(weight_offset), _ptr(out), _ptr(residual_out), _ptr(scales),
                                         x.numel() // width, width, _b.DTYPES[act], _b.DTYPES[wdt], QUANT[quant], st)
@@ -202,13 +211,13 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     T, Hq, D = q.shape
     Hkv, dev = k.shape[1], q.device
-    _b._need(q, "q", act, (T, Hq, D), dev)
-    _b._need(k, "k", act, (T, Hkv, D), dev)
-    _b._need(positions, "positions", torch.int32, (T,), dev)
+    _need(q, "q", act, (T, Hq, D), dev)
+    _need(k, "k", act, (T, Hkv, D), dev)
+    _need(positions, "positions", torch.int32, (T,), dev)
     _cuda(inv_freq, "inv_freq")
     if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
         raise ValueError(f"inv_freq must be [rotary / 2] with rotary <= {D} (got {tuple(inv_freq.shape)})")
-    _b._need(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
+    _need(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
     rows = 0
     if (k_cache is None) != (v_cache is None) or (k_cache is None) != (slots is None) or \
             (k_cache is None) != (v is None):
@@ -218,20 +227,20 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
         if k_cache.dim() != 4:
             raise ValueError("k_cache and v_cache must be [P, page_size, Hkv, D]")
         cshape = (k_cache.shape[0], k_cache.shape[1], Hkv, D)
-        _b._need(v, "v", act, (T, Hkv, D), dev)
-        _b._need(k_cache, "k_cache", act, cshape, dev)
-        _b._need(v_cache, "v_cache", act, cshape, dev)
-        _b._need(slots, "slots", torch.int32, (T,), dev)
+        _need(v, "v", act, (T, Hkv, D), dev)
+        _need(k_cache, "k_cache", act, cshape, dev)
+        _need(v_cache, "v_cache", act, cshape, dev)
+        _need(slots, "slots", torch.int32, (T,), dev)
         rows = cshape[0] * cshape[1]
     if q_out is not None:
-        _b._need(q_out, "q_out", act, (T, Hq, D), dev)
+        _need(q_out, "q_out", act, (T, Hq, D), dev)
     if k_out is not None:
-        _b._need(k_out, "k_out", act, (T, Hkv, D), dev)
+        _need(k_out, "k_out", act, (T, Hkv, D), dev)
     with _place(dev, stream) as st:
         if q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=act, device=dev)
+            q_out = torch.empty_like(q)
         if k_out is None and k_cache is None:
-            k_out = torch.empty(T, Hkv, D, dtype=act, device=dev)
+            k_out = torch.empty_like(k)
         rc = _layers_lib().gdn_rope_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(slots),
                                         float(mscale), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), T, Hq,
                                         Hkv, D, 2 * inv_freq.shape[0], int(bool(interleaved)), rows, _b.DTYPES[act],
@@ -274,28 +283,28 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
     max_pages = block_table.shape[1]
-    _b._need(q, "q", act, (B, Hq, D), dev)
-    _b._need(k_cache, "k_cache", act, (P, page, Hkv, D), dev)
-    _b._need(v_cache, "v_cache", act, (P, page, Hkv, D), dev)
-    _b._need(block_table, "block_table", torch.int32, (B, max_pages), dev)
-    _b._need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _need(q, "q", act, (B, Hq, D), dev)
+    _need(k_cache, "k_cache", act, (P, page, Hkv, D), dev)
+    _need(v_cache, "v_cache", act, (P, page, Hkv, D), dev)
+    _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
     if out is not None:
-        _b._need(out, "out", act, (B, Hq, D), dev)
+        _need(out, "out", act, (B, Hq, D), dev)
     if lse is not None:
-        _b._need(lse, "lse", torch.float32, (B, Hq), dev)
+        _need(lse, "lse", torch.float32, (B, Hq), dev)
     if workspace is not None:
         _cuda(workspace, "workspace")
         if workspace.device != dev or not workspace.is_contiguous():
             raise RuntimeError(f"workspace must be a contiguous tensor on {dev}")
     with _place(dev, stream) as st:
         if out is None:
-            out = torch.empty(B, Hq, D, dtype=act, device=dev)
+            out = torch.empty_like(q)
         if lse is None and output_lse:
-            lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+            lse = q.new_empty((B, Hq), dtype=torch.float32)
         if workspace is None:
             nbytes = paged_attn_workspace_bytes(B, Hq, Hkv, D, page, max_pages, int(max_seqlen))
             if nbytes:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+                workspace = q.new_empty((nbytes,), dtype=torch.uint8)
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         sc = 0.0 if scale is None else float(scale)
         rc = _layers_lib().gdn_paged_attn_fwd(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),

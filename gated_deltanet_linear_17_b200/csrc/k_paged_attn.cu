@@ -6,14 +6,20 @@
 // G flops a byte of a 16-bit cache, so up to G of about 250 the cache's bytes bound it, and the matrix
 // products (mma.sync: 16 query rows, zero-padded, against 8 keys or columns) only have to keep up.
 //
-// The split.  A CTA takes one piece of one sequence's keys for one key/value head and up to 16 of its
-// query heads; its four warps take every fourth tile of 16 keys.  A warp is on its own until the end
-// of the piece: its own ring of tiles in shared memory, filled by cp.async a few tiles ahead, its own
-// running maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end the
-// four partial results are joined through shared memory.  A sequence in one piece is then done;
-// otherwise the piece's unnormalised sum, maximum and sum of exponentials go to the workspace, and a
-// second kernel (started early by a programmatic dependency) joins the pieces in their order, so that
-// the result does not depend on the order in which CTAs run.
+// The split.  The work is one list of units of 64 keys, ordered by sequence, then by key/value head
+// (and group of 16 query heads), then along the keys.  The grid fills the GPU once and CTA i of C takes
+// the i-th of C equal parts of the list, whatever the lengths are: a long sequence is cut over many
+// CTAs, short ones share one.  Every CTA finds its part by a scan over the lengths, so nothing about them
+// has to be known on the host.  A part covers the end of one (sequence, head) pair, whole pairs, and
+// the beginning of another.  Whole pairs are written out; an incomplete one leaves its unnormalised sum,
+// maximum and sum of exponentials in one of the CTA's two places in the workspace, and a second kernel
+// (started early by a programmatic dependency) joins a pair's pieces in their order, so the result does
+// not depend on the order in which CTAs run.
+//
+// Inside a CTA four warps take every fourth tile of 16 keys.  A warp is on its own until the end of the
+// piece: its own ring of tiles in shared memory, filled by cp.async a few tiles ahead, its own running
+// maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end of a piece the
+// four partial results are joined through shared memory.
 //
 // Roundings.  Scores, exponentials (base 2, the scale folded in), sums and outputs are fp32.  The
 // probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
@@ -29,20 +35,24 @@ namespace gdn {
 
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 16;  // keys a warp takes at a time
-constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+constexpr float kLn2 = 0.693147181f;
 
-template <int D>
+// NT: octets of query rows (1 or 2)
+template <int D, int NT>
 struct Shape {
-    static constexpr int kStages = D == 256 ? 3 : 4;
+    static constexpr int kWarps = D == 256 ? 2 : 4, kThreads = 32 * kWarps;
+    static constexpr int kStages = D == 64 ? 4 : 3;
     static constexpr int kHalf = kTile * D * 2;      // bytes of a tile's keys (or values)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kRing = kStages * kStage;   // per warp
-    static constexpr int kQ = 16 * D * 2;            // query rows, behind the rings
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kQ = kRows * D * 2;         // query rows, behind the rings
     static constexpr int kSmem = kWarps * kRing + kQ;
-    static constexpr int kCtas = D == 256 ? 1 : D == 128 ? 1 : 2;
-    static_assert(kWarps * kRing >= kWarps * 16 * D * 4, "the join of the warps fits into the rings");
+    static constexpr bool kQInRegs = D * NT < 512;   // query fragments stay in registers
+    static constexpr int kSum = D + 4;               // floats of a row in the join of the warps: the four rows that
+                                                     // a quad writes lie 8 banks apart
+    static_assert(kWarps * kRing >= kWarps * kRows * kSum * 4, "the join of the warps fits into the rings");
 };
 
 // byte offset of 16-byte chunk c of row r in a tile of D-element rows: eight rows at one chunk lie in
@@ -60,6 +70,11 @@ __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, ui
     else mma16816_bf16(d, a, b0, b1);
 }
 
+__device__ __forceinline__ void ldsm_x2(uint32_t addr, uint32_t &r0, uint32_t &r1)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r0), "=r"(r1) : "r"(addr));
+}
+
 __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -71,43 +86,106 @@ __device__ __forceinline__ float quad_sum(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-// the pieces of a sequence of n keys: keys a piece, and pieces (1 for n = 0)
-__device__ __forceinline__ int2 pieces(int n, const AttnPlan &plan)
-{
-    const int least = ((n + plan.splits - 1) / plan.splits + 63) & ~63;
-    const int chunk = max(plan.chunk, least);
-    return make_int2(chunk, max(1, (n + chunk - 1) / chunk));
-}
 // a length outside the table's range stands for the whole sequence being refused
 __device__ __forceinline__ bool bad_length(int n, const AttnParams &p)
 {
     return n < 0 || n > (long long)p.max_pages * p.page_size;
 }
-
-template <int D, bool F16>
-__global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) paged_attn_kernel(const AttnParams p)
+// units of one head of a sequence; one without keys (or refused) has one, for its output row
+__device__ __forceinline__ int units(int n, const AttnParams &p)
 {
-    using S = Shape<D>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int b = (int)fast_div(blockIdx.x, p.by_splits), piece = blockIdx.x - b * p.plan.splits;
-    const int hkv = blockIdx.y / p.row_tiles, tile_row0 = (blockIdx.y - hkv * p.row_tiles) * 16;
-    const int rows = min(16, p.group - tile_row0);
-    const int head0 = hkv * p.group + tile_row0;  // first query head of this CTA
-    const int n_raw = p.lens[b];
-    const bool bad = bad_length(n_raw, p);
-    const int n = bad ? 0 : n_raw;
-    const int2 pc = pieces(n, p.plan);
-    if (piece >= pc.y) return;
-    const int k0 = piece * pc.x, k1 = min(n, k0 + pc.x);
+    return bad_length(n, p) || n == 0 ? 1 : (n + kAttnUnit - 1) / kAttnUnit;
+}
 
+// where a CTA's part of the list begins, and the list's length
+struct Part {
+    long long first, total;
+    int ctas;        // CTAs that have a part: the grid, or fewer where there are fewer units (so that no part in
+                     // between is empty and a pair's pieces lie in neighbouring CTAs)
+    int b;       // sequence of the first unit
+    long long rest;  // units before it in its sequence, over all heads
+};
+
+// All threads call it.  Thread t sums the units of its run of sequences; a scan over the threads finds the
+// run that holds the CTA's first unit, and the run's thread the sequence.
+template <int kThreads>
+__device__ __forceinline__ Part find_part(const AttnParams &p)
+{
+    constexpr int kWarps = kThreads / 32;
+    __shared__ long long warp_total[kWarps];
+    __shared__ Part found;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int run = (p.B + kThreads - 1) / kThreads, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
+    const int heads = p.Hkv * p.row_tiles;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units(p.lens[b], p);
+    long long upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += y;
+    }
+    if (lane == 31) warp_total[warp] = upto;
+    __syncthreads();
+    long long total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += warp_total[w];
+        total += warp_total[w];
+    }
+    total *= heads;
+    const int ctas = (int)min(total, (long long)gridDim.x);
+    const long long first = total * blockIdx.x / ctas;  // past the list for a CTA without a part
+    const long long begin = (upto - mine) * heads;
+    if (first >= begin && first < upto * heads) {
+        long long rest = first - begin;
+        int b = b0;
+        for (long long n; rest >= (n = (long long)units(p.lens[b], p) * heads); ++b) rest -= n;
+        found = Part{first, total, ctas, b, rest};
+    }
+    if (tid == 0 && (int)blockIdx.x >= ctas) found.ctas = ctas;
+    __syncthreads();
+    return found;
+}
+
+template <int D, int NT, bool F16>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) paged_attn_kernel(const AttnParams p)
+{
+    using S = Shape<D, NT>;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+    asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const uint32_t qs = smem_addr(smem) + kWarps * S::kRing;
     const uint16_t *kc = static_cast<const uint16_t *>(p.k), *vc = static_cast<const uint16_t *>(p.v);
+    const int heads = p.Hkv * p.row_tiles;
+
+    const Part part = find_part<kThreads>(p);
+    if ((int)blockIdx.x >= part.ctas) {
+        if (tid == 0) p.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
+        return;
+    }
+    long long left_units = part.total * (blockIdx.x + 1) / part.ctas - part.first;
+    int b = part.b, n_raw = p.lens[b], u_all = units(n_raw, p);
+    int pair = (int)(part.rest / u_all), u0 = (int)(part.rest - (long long)pair * u_all);
+    long long pos = part.first;
+    int4 begun = make_int4(0, 0, 0, 0);
+
+    for (;;) {
+    // this piece: units [u0, u0 + take) of head group `pair` of sequence b
+    const int take = (int)min(left_units, (long long)(u_all - u0));
+    const bool whole = take == u_all;
+    const bool bad = bad_length(n_raw, p);
+    const int n = bad ? 0 : n_raw;
+    const int hkv = pair / p.row_tiles, tile_row0 = (pair - hkv * p.row_tiles) * kRows;
+    const int rows = min(kRows, p.group - tile_row0);
+    const int head0 = hkv * p.group + tile_row0;  // first query head of this piece
+    const int k0 = u0 * kAttnUnit, k1 = min(n, (u0 + take) * kAttnUnit);
 
     // query rows to shared memory (rows past the group's zero)
-    for (int i = tid; i < 16 * (D / 8); i += kThreads) {
+    for (int i = tid; i < kRows * (D / 8); i += kThreads) {
         const int r = i / (D / 8), c = i % (D / 8);
         uint4 x = make_uint4(0, 0, 0, 0);
         if (r < rows)
@@ -145,14 +223,27 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) paged_attn_kernel(c
         }
     };
 
-    float o[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    // o: the output transposed, o[t][r][e] at column 16 t + lane / 4 (+ 8 for e >= 2) of query row 8 r + 2 (lane % 4)
+    // (+ 1 for odd e); m, l: of query row 8 r + lane / 4 (l this lane's part of the sum)
+    float o[D / 16][NT][4], m[NT], l[NT];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    uint32_t qf[D < 256 ? D / 16 : 1][4];
-    if (D < 256) {
+    for (int r = 0; r < NT; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-            ldsm_x4(qs + sw<D>(lane & 15, 2 * k + (lane >> 4)), qf[k][0], qf[k][1], qf[k][2], qf[k][3]);
+        for (int t = 0; t < D / 16; ++t) o[t][r][0] = o[t][r][1] = o[t][r][2] = o[t][r][3] = 0.f;
+    }
+    auto query = [&](int k, uint32_t (&a)[4]) {  // 16 columns of the query rows (rows 8 .. 15 zero when NT is 1)
+        if (NT == 2) ldsm_x4(qs + sw<D>(lane & 15, 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
+        else {
+            ldsm_x2(qs + sw<D>(lane & 7, 2 * k + ((lane >> 3) & 1)), a[0], a[2]);
+            a[1] = a[3] = 0;
+        }
+    };
+    uint32_t qf[S::kQInRegs ? D / 16 : 1][4];
+    if (S::kQInRegs) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) query(k, qf[k]);
     }
 
 #pragma unroll
@@ -174,76 +265,82 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) paged_attn_kernel(c
         const uint32_t ks = ring + stage * S::kStage, vs = ks + S::kHalf;
         stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
-        // scores of 16 rows x 16 keys
-        float s[2][4] = {};
+        // scores of the query rows against 16 keys; even and odd steps apart, to halve the chain of additions
+        float s[2][4] = {}, s1[2][4] = {};
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            uint32_t b0, b1, b2, b3, a[4];
+            uint32_t b0, b1, b2, b3;
             ldsm_x4(ks + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b0, b1, b2, b3);
-            if (D < 256) {
-                mma<F16>(s[0], qf[k], b0, b1);
-                mma<F16>(s[1], qf[k], b2, b3);
-            } else {
-                ldsm_x4(qs + sw<D>(lane & 15, 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
-                mma<F16>(s[0], a, b0, b1);
-                mma<F16>(s[1], a, b2, b3);
-            }
+            if (!S::kQInRegs) query(k, qf[0]);
+            const uint32_t *a = qf[S::kQInRegs ? k : 0];
+            mma<F16>(k & 1 ? s1[0] : s[0], a, b0, b1);
+            mma<F16>(k & 1 ? s1[1] : s[1], a, b2, b3);
         }
         const int left = k1 - (k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. 16, or more)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < 2 * NT; ++e) {
                 const int key = 8 * t + 2 * (lane & 3) + (e & 1);
-                s[t][e] = key < left ? s[t][e] * p.scale_log2 : -INFINITY;
+                s[t][e] = key < left ? (s[t][e] + s1[t][e]) * p.scale_log2 : -INFINITY;
             }
-        float alpha[2], ref[2];
+        float alpha[NT], ref[NT];
+        bool moved = false;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < NT; ++r) {
             const float top =
                 quad_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])));
             const float now = fmaxf(m[r], top);
             ref[r] = now == -INFINITY ? 0.f : now;  // every score -infinity so far: the exponentials are 0
             alpha[r] = exp2f(m[r] - ref[r]);
+            moved |= alpha[r] != 1.f;
             m[r] = now;
             l[r] *= alpha[r];
         }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+        if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int t = 0; t < D / 8; ++t) {
-                o[t][0] *= alpha[0];
-                o[t][1] *= alpha[0];
-                o[t][2] *= alpha[1];
-                o[t][3] *= alpha[1];
+            for (int r = 0; r < NT; ++r) {
+                const float a0 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3));
+                const float a1 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3) + 4);
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    o[t][r][0] *= a0;
+                    o[t][r][1] *= a1;
+                    o[t][r][2] *= a0;
+                    o[t][r][3] *= a1;
+                }
             }
         }
-        uint32_t hi[4], lo[4];
+        // The scores' fragment (query row lane / 4, keys 2 (lane % 4) + ..) is, packed, the second operand of
+        // V^T P^T (its column lane / 4, its rows 2 (lane % 4) + ..): no exchange between lanes.
+        uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int r = 0; r < NT; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
+            for (int t = 0; t < 2; ++t) {
                 const float p0 = exp2f(s[t][2 * r] - ref[r]), p1 = exp2f(s[t][2 * r + 1] - ref[r]);
                 l[r] += p0 + p1;
-                split2<F16>(p0, p1, hi[2 * t + r], lo[2 * t + r]);
+                split2<F16>(p0, p1, hi[r][t], lo[r][t]);
             }
 #pragma unroll
         for (int t = 0; t < D / 16; ++t) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4_t(vs + sw<D>((lane & 7) + (((lane >> 3) & 1) << 3), 2 * t + (lane >> 4)), b0, b1, b2, b3);
-            mma<F16>(o[2 * t], hi, b0, b1);
-            mma<F16>(o[2 * t + 1], hi, b2, b3);
-            mma<F16>(o[2 * t], lo, b0, b1);
-            mma<F16>(o[2 * t + 1], lo, b2, b3);
+            uint32_t a[4];
+            ldsm_x4_t(vs + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
+#pragma unroll
+            for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][0], hi[r][1]);
+#pragma unroll
+            for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][0], lo[r][1]);
         }
     }
     cp_async_wait<0>();
-    if (__any_sync(0xffffffffu, bad_page)) l[0] = l[1] = NAN;
-    if (bad) l[0] = l[1] = NAN;
-
-    // join the four warps
-    __shared__ float wm[kWarps][16], wl[kWarps][16];
+    if (__any_sync(0xffffffffu, bad_page) || bad) {
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < NT; ++r) l[r] = NAN;
+    }
+
+    // join the warps
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
         l[r] = quad_sum(l[r]);
         if ((lane & 3) == 0) {
             wm[warp][lane / 4 + 8 * r] = m[r];
@@ -252,88 +349,115 @@ __global__ void __launch_bounds__(kThreads, Shape<D>::kCtas) paged_attn_kernel(c
     }
     __syncthreads();  // every warp is done with its ring
     float *os = reinterpret_cast<float *>(smem);
-    float f[2];
+    auto top_of = [&](int row) {
+        float top = wm[0][row];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = lane / 4 + 8 * r;
-        const float top = fmaxf(fmaxf(wm[0][row], wm[1][row]), fmaxf(wm[2][row], wm[3][row]));
-        f[r] = exp2f(m[r] - (top == -INFINITY ? 0.f : top));
-    }
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wm[w][row]);
+        return top == -INFINITY ? 0.f : top;
+    };
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        const int row = lane / 4 + 8 * r;
-        if (row >= rows) continue;
+    for (int r = 0; r < NT; ++r)
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t)
-            *reinterpret_cast<float2 *>(os + (warp * 16 + row) * D + 8 * t + 2 * (lane & 3)) =
-                make_float2(o[t][2 * r] * f[r], o[t][2 * r + 1] * f[r]);
-    }
+        for (int e = 0; e < 2; ++e) {
+            const int row = 8 * r + 2 * (lane & 3) + e;
+            if (row >= rows) continue;
+            const float f = exp2f(wm[warp][row] - top_of(row));
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                float *at = os + (warp * kRows + row) * S::kSum + 16 * t + lane / 4;
+                at[0] = o[t][r][e] * f;
+                at[8] = o[t][r][2 + e] * f;
+            }
+        }
     __syncthreads();
     for (int i = tid; i < rows * (D / 4); i += kThreads) {
         const int row = i / (D / 4), c = i % (D / 4);
-        const float top = fmaxf(fmaxf(wm[0][row], wm[1][row]), fmaxf(wm[2][row], wm[3][row]));
+        const float top = top_of(row);
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         float sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float4 y = reinterpret_cast<const float4 *>(os + (w * 16 + row) * D)[c];
+            const float4 y = reinterpret_cast<const float4 *>(os + (w * kRows + row) * S::kSum)[c];
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            sum += wl[w][row] * exp2f(wm[w][row] - (top == -INFINITY ? 0.f : top));
+            sum += wl[w][row] * exp2f(wm[w][row] - top);
         }
-        const int head = head0 + row;
-        if (pc.y == 1) {
+        if (whole) {
+            const long long at = (long long)b * p.Hq + head0 + row;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            uint16_t *out = static_cast<uint16_t *>(p.out) + ((long long)b * p.Hq + head) * D + 4 * c;
-            *reinterpret_cast<uint2 *>(out) =
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
                 make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-            if (p.lse && c == 0) p.lse[(long long)b * p.Hq + head] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+            if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
         } else {
-            const long long at = ((long long)b * p.plan.splits + piece) * p.Hq + head;
+            // place 1: the pair begins here; place 0: it began in an earlier CTA
+            const long long at = (2LL * blockIdx.x + (u0 == 0)) * 16 + row;
             reinterpret_cast<float4 *>(p.part + at * D)[c] = x;
             if (c == 0) p.part_ml[at] = make_float2(top, sum);
         }
     }
+    if (!whole && u0 == 0) {
+        // the CTA that holds the pair's last unit u: the largest i with floor(i total / ctas) <= u
+        const long long last = pos + u_all - 1;
+        const int until = (int)(((last + 1) * part.ctas - 1) / part.total);
+        begun = make_int4(b, head0, rows, until - (int)blockIdx.x + 1);
+    }
+    left_units -= take;
+    if (left_units == 0) break;
+    pos += take;
+    u0 = 0;
+    if (++pair == heads) {
+        pair = 0;
+        ++b;
+        n_raw = p.lens[b];
+        u_all = units(n_raw, p);
+    }
+    __syncthreads();  // the rings, the query rows and wm, wl are free again
+    }
+    if (tid == 0) p.begun[blockIdx.x] = begun;
 }
 
-// joins the pieces of one (sequence, query head); nothing to do where the sequence was one piece
+// Joins the pieces of the pair that CTA blockIdx.x of the first kernel began and did not finish, one query
+// head a CTA: piece 0 lies in that CTA's place 1, piece j in place 0 of the j-th CTA after it.
+constexpr int kJoinThreads = 512;
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(128) paged_attn_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const AttnParams p)
 {
-    constexpr int kCols = D / 4, kGroups = 128 / kCols;  // threads along the columns, groups along the pieces
-    __shared__ float weight[GDN_ATTN_MAX_SPLITS];
-    __shared__ float red[2][4];
+    constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;  // threads along the columns, groups along the pieces
+    constexpr int kJoinWarps = kJoinThreads / 32;
+    __shared__ float weight[kAttnMaxCtas];
+    __shared__ float red[2][kJoinWarps];
     __shared__ float4 part[kGroups][kCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    const int n = p.lens[b];
-    if (bad_length(n, p)) return;
-    const int count = pieces(n, p.plan).y;
-    if (count == 1) return;
-    const long long at0 = (long long)b * p.plan.splits * p.Hq + head;
+    const int first = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    const int4 begun = p.begun[first];
+    const int count = begun.w;
+    if (count == 0 || row >= begun.z) return;
+    const auto place = [&](int j) { return (2LL * (first + j) + (j == 0)) * 16 + row; };
     float top = -INFINITY;
-    for (int s = tid; s < count; s += 128) top = fmaxf(top, p.part_ml[at0 + (long long)s * p.Hq].x);
+    for (int j = tid; j < count; j += kJoinThreads) top = fmaxf(top, p.part_ml[place(j)].x);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     if (lane == 0) red[0][tid >> 5] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
     float sum = 0.f;
-    for (int s = tid; s < count; s += 128) {
-        const float2 ml = p.part_ml[at0 + (long long)s * p.Hq];
+    for (int j = tid; j < count; j += kJoinThreads) {
+        const float2 ml = p.part_ml[place(j)];
         const float w = exp2f(ml.x - (top == -INFINITY ? 0.f : top));
-        weight[s] = w;
+        weight[j] = w;
         sum += w * ml.y;
     }
     sum = warp_sum(sum);
     if (lane == 0) red[1][tid >> 5] = sum;
     __syncthreads();
-    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    sum = 0.f;
+    for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
     const int c = tid % kCols, g = tid / kCols;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = g; s < count; s += kGroups) {
-        const float4 y = reinterpret_cast<const float4 *>(p.part + (at0 + (long long)s * p.Hq) * D)[c];
-        const float w = weight[s];
+#pragma unroll 8
+    for (int j = g; j < count; j += kGroups) {
+        const float4 y = reinterpret_cast<const float4 *>(p.part + place(j) * D)[c];
+        const float w = weight[j];
         x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
     }
     part[g][c] = x;
@@ -344,25 +468,25 @@ __global__ void __launch_bounds__(128) paged_attn_join_kernel(const AttnParams p
         const float4 y = part[i][c];
         x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
+    const long long at = (long long)begun.x * p.Hq + begun.y + row;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    uint16_t *out = static_cast<uint16_t *>(p.out) + ((long long)b * p.Hq + head) * D + 4 * c;
-    *reinterpret_cast<uint2 *>(out) = make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-    if (p.lse && c == 0) p.lse[(long long)b * p.Hq + head] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
+        make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
+    if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
 }
 
-template <int D, bool F16>
+template <int D, int NT, bool F16>
 cudaError_t launch(const AttnParams &p, cudaStream_t st)
 {
-    using S = Shape<D>;
-    const auto kern = paged_attn_kernel<D, F16>;
+    using S = Shape<D, NT>;
+    const auto kern = paged_attn_kernel<D, NT, F16>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)p.B * p.plan.splits, (unsigned)p.Hkv * p.row_tiles);
-    kern<<<grid, kThreads, S::kSmem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || p.plan.splits == 1) return e;
+    kern<<<(unsigned)p.ctas, S::kThreads, S::kSmem, st>>>(p);
+    if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.B, (unsigned)p.Hq);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(16, p.group));
+    cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -374,25 +498,25 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
 
 }  // namespace
 
-AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len)
+int attn_ctas(int B, int Hq, int Hkv, int D, long long max_len)
 {
-    const long long rows = (Hq / Hkv + 15) / 16;
-    const long long pairs = (long long)B * Hkv * rows, slots = 148 * (D == 64 ? 2 : 1);
-    long long chunk = (max_len * pairs + slots - 1) / slots;
-    if (pairs >= slots / 2) chunk = max_len * pairs / (8 * slots);
-    chunk = std::max(chunk, 256LL);
-    chunk = std::max(chunk, (max_len + GDN_ATTN_MAX_SPLITS - 1) / GDN_ATTN_MAX_SPLITS);
-    chunk = (chunk + 63) / 64 * 64;
-    const long long splits = std::max(1LL, (max_len + chunk - 1) / chunk);
-    return AttnPlan{(int)splits, (int)chunk};
+    const long long heads = (long long)Hkv * ((Hq / Hkv + 15) / 16);
+    const long long most = (long long)B * heads * std::max(1LL, (max_len + kAttnUnit - 1) / kAttnUnit);
+    return (int)std::min<long long>(most, kAttnSms * kAttnCtasPerSm(D));
+}
+
+template <int D, bool F16>
+cudaError_t launch_rows(const AttnParams &p, cudaStream_t st)
+{
+    return p.group <= 8 ? launch<D, 1, F16>(p, st) : launch<D, 2, F16>(p, st);
 }
 
 cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, cudaStream_t st)
 {
     switch (D) {
-    case 64: return f16 ? launch<64, true>(p, st) : launch<64, false>(p, st);
-    case 128: return f16 ? launch<128, true>(p, st) : launch<128, false>(p, st);
-    default: return f16 ? launch<256, true>(p, st) : launch<256, false>(p, st);
+    case 64: return f16 ? launch_rows<64, true>(p, st) : launch_rows<64, false>(p, st);
+    case 128: return f16 ? launch_rows<128, true>(p, st) : launch_rows<128, false>(p, st);
+    default: return f16 ? launch_rows<256, true>(p, st) : launch_rows<256, false>(p, st);
     }
 }
 

@@ -50,24 +50,25 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams &p, int act_dtype, bool interleaved, cudaStream_t st);
 
-// How the cache's length is split over CTAs: sequence b's keys fall into pieces of max(chunk,
-// ceil(len / splits) rounded up to 64) keys, so there are never more than `splits` pieces.
-struct AttnPlan {
-    int splits, chunk;
-};
-AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len);
+// The paged attention's grid: CTAs that fill a B200 (148 SMs) once, or one for each unit of kAttnUnit
+// keys where max_len (the longest sequence that the caller expects) leaves fewer; any count is right.
+constexpr int kAttnUnit = 64, kAttnSms = 148;
+constexpr int kAttnCtasPerSm(int D) { return D == 64 ? 3 : 2; }
+constexpr int kAttnMaxCtas = kAttnSms * 3;
+int attn_ctas(int B, int Hq, int Hkv, int D, long long max_len);
 
 struct AttnParams {
     const void *q, *k, *v;
     const int32_t *table, *lens;
     void *out;
     float *lse;
-    float *part;      // [B][splits][Hq][D] unnormalised sums
-    float2 *part_ml;  // [B][splits][Hq]: running maximum (base 2) and sum
+    int4 *begun;      // [ctas]: sequence, first query head, query heads and pieces of the pair that a CTA began and
+                      // did not finish (pieces 0: none)
+    float2 *part_ml;  // [ctas][2][16]: a piece's maximum (base 2) and sum of exponentials
+    float *part;      // [ctas][2][16][D]: its unnormalised sum
     float scale_log2;
-    int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages;
-    AttnPlan plan;
-    FastDiv by_page, by_splits;
+    int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages, ctas;
+    FastDiv by_page;
 };
 cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, cudaStream_t st);
 

@@ -36,7 +36,6 @@ extern "C" {
 #define GDN_QUANT_GROUP 128
 #define GDN_NORM_MAX_WIDTH 32768
 #define GDN_ROPE_MAX_DIM 512
-#define GDN_ATTN_MAX_SPLITS 256
 
 /*
  * gdn_rms_norm -- root-mean-square norm of each row.
@@ -133,8 +132,8 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  *                 zero row and lse = -infinity
  *   scale         <= 0 selects 1/sqrt(D)
  *   out           [B, Hq, D] of act_dtype; lse fp32 [B, Hq] or NULL
- *   max_seqlen    the longest sequence if known, else 0: sets how the work is
- *                 split; any value gives a right result
+ *   max_seqlen    the longest sequence if known, else 0: keeps the grid and the
+ *                 workspace of a small call small; any value gives a right result
  *   D             64, 128 or 256; Hq a multiple of Hkv; page_size >= 1
  *   workspace     >= gdn_paged_attn_workspace_bytes(...) for the same sizes and
  *                 max_seqlen, 16-byte aligned, or NULL: the call then allocates
