@@ -91,24 +91,29 @@ __device__ __forceinline__ bool bad_length(int n, const AttnParams &p)
 {
     return n < 0 || n > (long long)p.max_pages * p.page_size;
 }
-// units of one head of a sequence; one without keys (or refused) has one, for its output row
-__device__ __forceinline__ int units(int n, const AttnParams &p)
+// Places that one head of a sequence takes in the list: one for each kAttnUnit keys, behind kLead<D>
+// that stand for what a pair costs beside its keys (its queries, the first page's latency, its output), so
+// that a CTA of many short pairs gets no more work than one of a long pair.
+template <int D>
+constexpr int kLead = D == 64 ? 3 : D == 128 ? 2 : 1;
+template <int D>
+__device__ __forceinline__ int places(int n, const AttnParams &p)
 {
-    return bad_length(n, p) || n == 0 ? 1 : (n + kAttnUnit - 1) / kAttnUnit;
+    return kLead<D> + (bad_length(n, p) ? 0 : (n + kAttnUnit - 1) / kAttnUnit);
 }
 
 // where a CTA's part of the list begins, and the list's length
 struct Part {
     long long first, total;
-    int ctas;        // CTAs that have a part: the grid, or fewer where there are fewer units (so that no part in
+    int ctas;        // CTAs that have a part: the grid, or fewer where there are fewer places (so that no part in
                      // between is empty and a pair's pieces lie in neighbouring CTAs)
-    int b;       // sequence of the first unit
-    long long rest;  // units before it in its sequence, over all heads
+    int b;           // sequence of the first place
+    long long rest;  // places before it in its sequence, over all heads
 };
 
-// All threads call it.  Thread t sums the units of its run of sequences; a scan over the threads finds the
-// run that holds the CTA's first unit, and the run's thread the sequence.
-template <int kThreads>
+// All threads call it.  Thread t sums the places of its run of sequences; a scan over the threads finds the
+// run that holds the CTA's first place, and the run's thread the sequence.
+template <int D, int kThreads>
 __device__ __forceinline__ Part find_part(const AttnParams &p)
 {
     constexpr int kWarps = kThreads / 32;
@@ -118,7 +123,7 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     const int run = (p.B + kThreads - 1) / kThreads, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
     const int heads = p.Hkv * p.row_tiles;
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units(p.lens[b], p);
+    for (int b = b0; b < b1; ++b) mine += places<D>(p.lens[b], p);
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -140,7 +145,7 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     if (first >= begin && first < upto * heads) {
         long long rest = first - begin;
         int b = b0;
-        for (long long n; rest >= (n = (long long)units(p.lens[b], p) * heads); ++b) rest -= n;
+        for (long long n; rest >= (n = (long long)places<D>(p.lens[b], p) * heads); ++b) rest -= n;
         found = Part{first, total, ctas, b, rest};
     }
     if (tid == 0 && (int)blockIdx.x >= ctas) found.ctas = ctas;
@@ -162,38 +167,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) pag
     const uint16_t *kc = static_cast<const uint16_t *>(p.k), *vc = static_cast<const uint16_t *>(p.v);
     const int heads = p.Hkv * p.row_tiles;
 
-    const Part part = find_part<kThreads>(p);
+    const Part part = find_part<D, kThreads>(p);
     if ((int)blockIdx.x >= part.ctas) {
         if (tid == 0) p.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
         return;
     }
-    long long left_units = part.total * (blockIdx.x + 1) / part.ctas - part.first;
-    int b = part.b, n_raw = p.lens[b], u_all = units(n_raw, p);
+    long long left_places = part.total * (blockIdx.x + 1) / part.ctas - part.first;
+    int b = part.b, n_raw = p.lens[b], u_all = places<D>(n_raw, p);
     int pair = (int)(part.rest / u_all), u0 = (int)(part.rest - (long long)pair * u_all);
     long long pos = part.first;
     int4 begun = make_int4(0, 0, 0, 0);
 
     for (;;) {
-    // this piece: units [u0, u0 + take) of head group `pair` of sequence b
-    const int take = (int)min(left_units, (long long)(u_all - u0));
+    // this piece: places [u0, u0 + take) of head group `pair` of sequence b
+    const int take = (int)min(left_places, (long long)(u_all - u0));
     const bool whole = take == u_all;
     const bool bad = bad_length(n_raw, p);
     const int n = bad ? 0 : n_raw;
     const int hkv = pair / p.row_tiles, tile_row0 = (pair - hkv * p.row_tiles) * kRows;
     const int rows = min(kRows, p.group - tile_row0);
     const int head0 = hkv * p.group + tile_row0;  // first query head of this piece
-    const int k0 = u0 * kAttnUnit, k1 = min(n, (u0 + take) * kAttnUnit);
-
-    // query rows to shared memory (rows past the group's zero)
-    for (int i = tid; i < kRows * (D / 8); i += kThreads) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-            x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                ((long long)b * p.Hq + head0 + r) * D)[c];
-        *reinterpret_cast<uint4 *>(smem + kWarps * S::kRing + sw<D>(r, c)) = x;
-    }
-    __syncthreads();
+    const int k0 = max(0, u0 - kLead<D>) * kAttnUnit, k1 = min(n, max(0, u0 + take - kLead<D>) * kAttnUnit);
+    const int n_next = b + 1 < p.B ? p.lens[b + 1] : 0;
 
     // this warp's tiles: first + 16 (warp + 4 i)
     const int tiles = (k1 - k0 + kTile - 1) / kTile;
@@ -223,6 +218,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) pag
         }
     };
 
+    // the first tiles are on their way before the queries are waited for
+    {
+        int row[S::kStages - 1];
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) row[i] = cache_row(i);
+#pragma unroll
+        for (int i = 0; i < S::kStages - 1; ++i) {
+            if (i < mine) fetch(i, row[i]);
+            cp_async_commit();
+        }
+    }
+    int next_row = cache_row(S::kStages - 1);
+    // query rows to shared memory (rows past the group's zero)
+    for (int i = tid; i < kRows * (D / 8); i += kThreads) {
+        const int r = i / (D / 8), c = i % (D / 8);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows)
+            x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
+                                                ((long long)b * p.Hq + head0 + r) * D)[c];
+        *reinterpret_cast<uint4 *>(smem + kWarps * S::kRing + sw<D>(r, c)) = x;
+    }
+    __syncthreads();
+
     // o: the output transposed, o[t][r][e] at column 16 t + lane / 4 (+ 8 for e >= 2) of query row 8 r + 2 (lane % 4)
     // (+ 1 for odd e); m, l: of query row 8 r + lane / 4 (l this lane's part of the sum)
     float o[D / 16][NT][4], m[NT], l[NT];
@@ -246,12 +264,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) pag
         for (int k = 0; k < D / 16; ++k) query(k, qf[k]);
     }
 
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) {
-        if (i < mine) fetch(i, cache_row(i));
-        cp_async_commit();
-    }
-    int next_row = cache_row(S::kStages - 1);
     int stage = 0;
     for (int i = 0; i < mine; ++i) {
         cp_async_wait<S::kStages - 2>();
@@ -395,84 +407,162 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) pag
         }
     }
     if (!whole && u0 == 0) {
-        // the CTA that holds the pair's last unit u: the largest i with floor(i total / ctas) <= u
+        // the CTA that holds the pair's last place u: the largest i with floor(i total / ctas) <= u
         const long long last = pos + u_all - 1;
         const int until = (int)(((last + 1) * part.ctas - 1) / part.total);
         begun = make_int4(b, head0, rows, until - (int)blockIdx.x + 1);
     }
-    left_units -= take;
-    if (left_units == 0) break;
+    left_places -= take;
+    if (left_places == 0) break;
     pos += take;
     u0 = 0;
     if (++pair == heads) {
         pair = 0;
         ++b;
-        n_raw = p.lens[b];
-        u_all = units(n_raw, p);
+        n_raw = n_next;
+        u_all = places<D>(n_raw, p);
     }
     __syncthreads();  // the rings, the query rows and wm, wl are free again
     }
     if (tid == 0) p.begun[blockIdx.x] = begun;
 }
 
-// Joins the pieces of the pair that CTA blockIdx.x of the first kernel began and did not finish, one query
-// head a CTA: piece 0 lies in that CTA's place 1, piece j in place 0 of the j-th CTA after it.
-constexpr int kJoinThreads = 512;
+// Joins the pieces of every pair that a CTA of the first kernel began and did not finish: piece 0 lies in
+// that CTA's place 1, piece j in place 0 of the j-th CTA after it.  Every CTA reads the list of such pairs;
+// a query head of a pair of few pieces is one warp's work, of many pieces (a long sequence cut over the whole
+// GPU) one CTA's for each 128 columns, its threads spread over the pieces.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = kAttnSms, kFewPieces = 4;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const AttnParams p)
 {
-    constexpr int kCols = D / 4, kGroups = kJoinThreads / kCols;  // threads along the columns, groups along the pieces
-    constexpr int kJoinWarps = kJoinThreads / 32;
-    __shared__ float weight[kAttnMaxCtas];
-    __shared__ float red[2][kJoinWarps];
+    constexpr int kBlock = D < 128 ? D : 128, kBlocks = D / kBlock;   // columns of a CTA's item, items of a row
+    constexpr int kCols = kBlock / 4, kGroups = kJoinThreads / kCols;  // threads along the columns, along the pieces
+    constexpr int kPer = (kAttnMaxCtas + kJoinThreads - 1) / kJoinThreads;
+    static_assert(kPer == 1, "a thread takes one CTA's record");
+    __shared__ int4 list[kAttnMaxCtas];
+    __shared__ uint32_t upto[kAttnMaxCtas], warp_total[kJoinWarps];  // many << 16 | few: items up to and with this one
+    __shared__ float weight[kAttnMaxCtas], red[2][kJoinWarps];
     __shared__ float4 part[kGroups][kCols];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int first = blockIdx.x, row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-    const int4 begun = p.begun[first];
-    const int count = begun.w;
-    if (count == 0 || row >= begun.z) return;
-    const auto place = [&](int j) { return (2LL * (first + j) + (j == 0)) * 16 + row; };
-    float top = -INFINITY;
-    for (int j = tid; j < count; j += kJoinThreads) top = fmaxf(top, p.part_ml[place(j)].x);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) red[0][tid >> 5] = top;
-    __syncthreads();
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
-    float sum = 0.f;
-    for (int j = tid; j < count; j += kJoinThreads) {
-        const float2 ml = p.part_ml[place(j)];
-        const float w = exp2f(ml.x - (top == -INFINITY ? 0.f : top));
-        weight[j] = w;
-        sum += w * ml.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint32_t sum_items = 0;
+    if (tid < p.ctas) {
+        const int4 r = p.begun[tid];
+        list[tid] = r;
+        if (r.w > 0) sum_items = r.w > kFewPieces ? (uint32_t)(r.z * kBlocks) << 16 : (uint32_t)r.z;
     }
-    sum = warp_sum(sum);
-    if (lane == 0) red[1][tid >> 5] = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, sum_items, d);
+        if (lane >= d) sum_items += y;
+    }
+    if (lane == 31) warp_total[warp] = sum_items;
     __syncthreads();
-    sum = 0.f;
-    for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
-    const int c = tid % kCols, g = tid / kCols;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    uint32_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+        if (w < warp) sum_items += warp_total[w];
+        total += warp_total[w];
+    }
+    if (tid < p.ctas) upto[tid] = sum_items;
+    __syncthreads();
+    const int many = total >> 16, few = total & 0xffff;
+    // record that holds item `item` of a kind, and the item's number in it
+    auto find = [&](int item, int shift, int *inner) {
+        int lo = 0, hi = p.ctas - 1;  // smallest record whose running count exceeds the item
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if ((int)(upto[mid] >> shift & 0xffff) > item) hi = mid;
+            else lo = mid + 1;
+        }
+        *inner = item - (lo ? (int)(upto[lo - 1] >> shift & 0xffff) : 0);
+        return lo;
+    };
+    auto write = [&](const int4 &rec, int row, int c, float4 x, float top, float sum) {  // 4 columns from 4 c on
+        const long long at = (long long)rec.x * p.Hq + rec.y + row;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
+            make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
+        if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+    };
+    auto place = [&](int first, int j, int row) { return (2LL * (first + j) + (j == 0)) * 16 + row; };
+
+    for (int item = warp * gridDim.x + blockIdx.x; item < few; item += gridDim.x * kJoinWarps) {
+        int row;
+        const int first = find(item, 0, &row);
+        const int4 rec = list[first];
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < rec.w) ml = p.part_ml[place(first, lane, row)];
+        float top = ml.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        top = top == -INFINITY ? 0.f : top;
+        const float w = exp2f(ml.x - top), sum = warp_sum(w * ml.y);
+        float wj[kFewPieces];
+#pragma unroll
+        for (int j = 0; j < kFewPieces; ++j) wj[j] = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+        for (int c = lane; c < D / 4; c += 32) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int j = 0; j < kFewPieces; ++j) {
+                if (j >= rec.w) break;
+                const float4 y = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[c];
+                x.x = fmaf(wj[j], y.x, x.x), x.y = fmaf(wj[j], y.y, x.y);
+                x.z = fmaf(wj[j], y.z, x.z), x.w = fmaf(wj[j], y.w, x.w);
+            }
+            write(rec, row, c, x, top, sum);
+        }
+    }
+
+    for (int item = blockIdx.x; item < many; item += gridDim.x) {
+        int inner;
+        const int first = find(item, 16, &inner), row = inner / kBlocks, block = inner % kBlocks;
+        const int4 rec = list[first];
+        const int count = rec.w;
+        float top = -INFINITY;
+        for (int j = tid; j < count; j += kJoinThreads) top = fmaxf(top, p.part_ml[place(first, j, row)].x);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        if (lane == 0) red[0][warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
+        top = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        for (int j = tid; j < count; j += kJoinThreads) {
+            const float2 ml = p.part_ml[place(first, j, row)];
+            const float w = exp2f(ml.x - top);
+            weight[j] = w;
+            sum += w * ml.y;
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) red[1][warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
+        const int c = block * kCols + tid % kCols, g = tid / kCols;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int j = g; j < count; j += kGroups) {
-        const float4 y = reinterpret_cast<const float4 *>(p.part + place(j) * D)[c];
-        const float w = weight[j];
-        x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
-    }
-    part[g][c] = x;
-    __syncthreads();
-    if (g != 0) return;
+        for (int j = g; j < count; j += kGroups) {
+            const float4 y = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[c];
+            const float w = weight[j];
+            x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
+        }
+        part[g][tid % kCols] = x;
+        __syncthreads();
+        if (g == 0) {
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) {
-        const float4 y = part[i][c];
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            for (int i = 1; i < kGroups; ++i) {
+                const float4 y = part[i][tid];
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+            }
+            write(rec, row, c, x, top, sum);
+        }
+        __syncthreads();
     }
-    const long long at = (long long)begun.x * p.Hq + begun.y + row;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
-        make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-    if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
 }
 
 template <int D, int NT, bool F16>
@@ -485,7 +575,7 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
     kern<<<(unsigned)p.ctas, S::kThreads, S::kSmem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)std::min(16, p.group));
+    cfg.gridDim = dim3(kJoinCtas);
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
