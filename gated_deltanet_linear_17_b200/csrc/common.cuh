@@ -40,6 +40,11 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool v
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n)
                  : "memory");
 }
+// 16-byte destination, n source bytes (0 .. 16), the rest zero
+__device__ __forceinline__ void cp_async16_part(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 // 4-byte global->shared copy (always valid)
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src)
 {

@@ -95,8 +95,8 @@ int gdn_rms_norm(const void *x, const void *residual, const void *gate, const vo
     p.x = x, p.residual = residual, p.gate = gate, p.weight = weight;
     p.out = out, p.residual_out = residual_out, p.scales = scales;
     p.eps = eps, p.weight_offset = weight_offset, p.inv_width = 1.0f / (float)width;
-    p.rows = rows, p.width = width, p.weight_f32 = weight_dtype != act_dtype;
-    return cuda_status(gdn::launch_rms_norm(p, act_dtype, quant, (cudaStream_t)stream));
+    p.rows = rows, p.width = width, p.quant = quant, p.weight_f32 = weight_dtype == GDN_DTYPE_FP32;
+    return cuda_status(gdn::launch_rms_norm(p, act_dtype, (cudaStream_t)stream));
 }
 
 int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *positions, const float *inv_freq,

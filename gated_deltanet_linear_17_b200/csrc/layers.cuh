@@ -45,6 +45,15 @@ struct Raw8 {
             x[2 * i + 1] = f.y;
         }
     }
+    __device__ __forceinline__ void up2(float2 (&x)[4]) const
+    {
+        x[0] = A::up2(w.x), x[1] = A::up2(w.y), x[2] = A::up2(w.z), x[3] = A::up2(w.w);
+    }
+    __device__ __forceinline__ void down2(const float2 (&x)[4])
+    {
+        w = make_uint4(A::down2(x[0].x, x[0].y), A::down2(x[1].x, x[1].y), A::down2(x[2].x, x[2].y),
+                       A::down2(x[3].x, x[3].y));
+    }
     __device__ __forceinline__ void down(const float (&x)[8])
     {
         w = make_uint4(A::down2(x[0], x[1]), A::down2(x[2], x[3]), A::down2(x[4], x[5]), A::down2(x[6], x[7]));
@@ -66,6 +75,16 @@ struct Raw8<F32> {
     __device__ __forceinline__ void up(float (&x)[8]) const
     {
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ __forceinline__ void up2(float2 (&x)[4]) const
+    {
+        x[0] = make_float2(a.x, a.y), x[1] = make_float2(a.z, a.w);
+        x[2] = make_float2(b.x, b.y), x[3] = make_float2(b.z, b.w);
+    }
+    __device__ __forceinline__ void down2(const float2 (&x)[4])
+    {
+        a = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+        b = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
     }
     __device__ __forceinline__ void down(const float (&x)[8])
     {

@@ -32,9 +32,10 @@ struct NormParams {
     float eps, weight_offset, inv_width;
     long long rows;
     int width;
+    int quant;        // GDN_QUANT_*
     bool weight_f32;
 };
-cudaError_t launch_rms_norm(const NormParams &p, int act_dtype, int quant, cudaStream_t st);
+cudaError_t launch_rms_norm(const NormParams &p, int act_dtype, cudaStream_t st);
 
 struct RopeParams {
     const void *q, *k, *v;
