@@ -112,33 +112,49 @@ __device__ __forceinline__ float weight_at(const NormParams &p, int c, bool f16)
 
 constexpr int kNarrowBlock = 128;  // threads of a CTA whose warps hold whole rows
 __host__ __device__ constexpr int norm_block(int L) { return L <= 32 ? kNarrowBlock : L; }
+// Columns a thread holds.  32 of a 16-bit type; 16 of fp32, whose elements have twice the time and take twice the
+// ring (1537 columns with residual and gate: 39 us with 32, 8 warps an SM).
+template <class A>
+__host__ __device__ constexpr int norm_per(int L) { return sizeof(typename A::raw) == 4 && L <= 512 ? 16 : 32; }
 // CTAs an SM that the registers leave room for
 __host__ __device__ constexpr int norm_ctas(int L) { return (L <= 256 ? 768 : 1024) / norm_block(L); }
 // Rows up to 8192 columns come through two stages in shared memory: cp.async brings a group's next row while it
 // works on this one.  A thread fetches what it will use itself, so no barrier orders the stages.  Wider rows go
 // straight to registers.
-__host__ __device__ constexpr bool norm_ring(Kind kind, int L) { return kind != kElements && L <= 256; }
-// Where warps hold whole rows, the weights lie in shared memory in fp32, offset added, one float of padding behind
-// every N: the lanes of a warp then read N columns apart from different banks.
+template <class A>
+__host__ __device__ constexpr bool norm_ring(Kind kind, int L) { return kind != kElements && L * norm_per<A>(L) <= 8192; }
+// Where warps hold whole rows, the weights lie in shared memory in fp32, offset added: in order (kFull), or
+// (kBlocks) as 2 N - 1 lines, line r of the weights r - (N - 1) behind the first of each unit, zeros outside the
+// row.  A unit of a row that begins ph elements into a block then reads N lines from N - 1 - ph on, its
+// neighbours beside it.
 __host__ __device__ constexpr bool norm_weights(Kind kind, int L) { return kind != kElements && L <= 32; }
-template <int N>
-__host__ __device__ constexpr int padded(int c) { return c + c / N; }
+template <class A>
+__host__ __device__ constexpr int norm_line(int L) { return L * norm_per<A>(L) / Unit<A>::N + 1; }
+template <class A>
+__host__ __device__ constexpr int norm_weight_bytes(Kind kind, int L)
+{
+    return !norm_weights(kind, L) ? 0
+           : kind == kFull        ? L * norm_per<A>(L) * 4
+                                  : ((2 * Unit<A>::N - 1) * norm_line<A>(L) * 4 + 15) / 16 * 16;
+}
+__host__ __device__ constexpr int pow2(int n) { return n <= 1 ? 1 : 2 * pow2((n + 1) / 2); }
 
-// A group of L threads strides over the rows; each of them holds 32 columns.
+// A group of L threads strides over the rows.
 template <class A, Kind KIND, int L>
 __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(const NormParams p)
 {
     using U = Unit<A>;
     using raw = typename A::raw;
-    constexpr bool kEl = KIND == kElements, kRing = norm_ring(KIND, L), kShared = norm_weights(KIND, L);
+    constexpr bool kEl = KIND == kElements, kRing = norm_ring<A>(KIND, L), kShared = norm_weights(KIND, L);
     constexpr bool kF16 = std::is_same<A, F16>::value;
-    constexpr int N = kEl ? 4 : U::N, H = N / 2, NV = 32 / N, W = L < 32 ? L : 32, kWarps = L / 32;
+    constexpr int N = kEl ? 4 : U::N, H = N / 2, PER = norm_per<A>(L), NV = PER / N;
+    constexpr int W = L < 32 ? L : 32, kWarps = pow2(L / 32);  // warps, rounded up for the shuffles
     constexpr int kBlock = norm_block(L), kRows = L <= 32 ? kBlock / L : 1, kStep = L * N;
     constexpr int kGroupLanes = kEl ? 32 : 128 / N;  // lanes that hold a group of 128 columns
     __shared__ float red[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int t = L <= 32 ? (int)threadIdx.x % L : (int)threadIdx.x;
-    const int width = KIND == kFull ? 32 * L : p.width, quant = p.quant;
+    const int width = KIND == kFull ? PER * L : p.width, quant = p.quant;
     const int v0 = kEl ? (t >> 5) * 128 + (t & 31) : t * N;  // place of this thread's first element, phase added
     const int first = (int)(L <= 32 ? blockIdx.x * kRows + threadIdx.x / L : blockIdx.x);
     const int stride = (int)gridDim.x * kRows, rows = (int)p.rows;
@@ -150,49 +166,57 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     auto phase = [&](int row) { return KIND == kBlocks ? (int)((long long)row * width) & (N - 1) : 0; };
 
     float *weights = reinterpret_cast<float *>(smem);
-    uint8_t *ring = smem + (kShared ? (padded<U::N>(32 * L) * 4 + 15) / 16 * 16 : 0);
+    uint8_t *ring = smem + norm_weight_bytes<A>(KIND, L);
+    constexpr int kLine = norm_line<A>(L);
     // this thread's 16 bytes of (stage, matrix, unit); matrices in the order x, residual, gate
     constexpr int kPlane = kBlock * 16, kMatrix = NV * kPlane;
     const int gate_at = residual ? 2 * kMatrix : kMatrix, stage_bytes = kMatrix * (1 + residual + gated);
     uint8_t *mine = ring + threadIdx.x * 16;
     const uint32_t mine_addr = smem_addr(mine);
+    // elements of the matrix from the row's first on (a block of its last rows may end behind them), as an int
+    auto rest_of = [&](int row) { return (int)min(end - (long long)row * width, 1LL << 20); };
     auto fetch = [&](int stage, int row) {
         if (row < rows) {
-            const int ph = phase(row);
-            const long long at = (long long)row * width - ph + v0;
+            const int c0 = v0 - phase(row), rest = KIND == kFull ? 0 : rest_of(row);
+            const long long at = (long long)row * width + c0;
+            const raw *fx = x + at, *fr = res + at, *fg = gate + at;
             const uint32_t dst = mine_addr + stage * stage_bytes;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
-                const int v = v0 + k * kStep;
-                if (KIND != kFull && v - ph >= width) continue;
-                const long long e = at + k * kStep;
-                // the last block of the matrix may be a part of one
-                const int bytes = KIND == kFull ? 16 : (int)min(16LL, (end - e) * (long long)sizeof(raw));
-                cp_async16_part(dst + k * kPlane, x + e, bytes);
-                if (residual) cp_async16_part(dst + kMatrix + k * kPlane, res + e, bytes);
-                if (gated) cp_async16_part(dst + gate_at + k * kPlane, gate + e, bytes);
+                const int c = c0 + k * kStep;
+                if (KIND != kFull && c >= width) continue;
+                const int bytes = KIND == kFull ? 16 : min(16, (rest - c) * (int)sizeof(raw));
+                cp_async16_part(dst + k * kPlane, fx + k * kStep, bytes);
+                if (residual) cp_async16_part(dst + kMatrix + k * kPlane, fr + k * kStep, bytes);
+                if (gated) cp_async16_part(dst + gate_at + k * kPlane, fg + k * kStep, bytes);
             }
         }
         cp_async_commit();
     };
-    // without a ring: the unit at element e (column c of its row) from memory
-    auto load = [&](const raw *m, long long e, int c) {
+    // Units from here on: m points at the unit's first element, c is its column, `in` whether the whole unit lies
+    // in the row.
+    auto load = [&](const raw *m, int c, int rest) {  // without a ring
         if constexpr (kEl) {
             uint32_t w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 w[j] = 0;
                 if (c + 32 * j < width) {
-                    if constexpr (sizeof(raw) == 2) w[j] = __float_as_uint(A::up(m[e + 32 * j]));
-                    else w[j] = __float_as_uint(m[e + 32 * j]);
+                    if constexpr (sizeof(raw) == 2) w[j] = __float_as_uint(A::up(m[32 * j]));
+                    else w[j] = __float_as_uint(m[32 * j]);
                 }
             }
             return make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-            if (KIND == kFull || e + N <= end) return *reinterpret_cast<const uint4 *>(m + e);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            for (int j = 0; e + j < end; ++j) reinterpret_cast<raw *>(&w)[j] = m[e + j];
-            return w;
+            if (KIND == kFull || c + N <= rest) return *reinterpret_cast<const uint4 *>(m);
+            uint32_t w[4] = {};
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (c + j < rest) {
+                    if constexpr (sizeof(raw) == 2) w[j / 2] |= (uint32_t)m[j] << 16 * (j & 1);
+                    else w[j] = __float_as_uint(m[j]);
+                }
+            return make_uint4(w[0], w[1], w[2], w[3]);
         }
     };
     auto up = [&](const uint4 &w, float2 (&v)[H]) {
@@ -203,65 +227,84 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             U::up(w, v);
         }
     };
-    // clears what is not in the row; c: column of the unit's first element
-    auto mask = [&](int c, float2 (&v)[H]) {
-        if (KIND != kBlocks || (c >= 0 && c + N <= width)) return;
+    auto mask = [&](int c, bool in, float2 (&v)[H]) {  // clears what is not in the row
+        if (KIND != kBlocks || in) return;
 #pragma unroll
         for (int j = 0; j < N; ++j)
-            if (c + j < 0 || c + j >= width) (j & 1 ? v[j / 2].y : v[j / 2].x) = 0.f;
+            if ((unsigned)(c + j) >= (unsigned)width) (j & 1 ? v[j / 2].y : v[j / 2].x) = 0.f;
     };
-    // e: the unit's first element in the matrix
-    auto store = [&](raw *m, long long e, int c, const float2 (&v)[H]) {
+    auto store = [&](raw *m, int c, bool in, const float2 (&v)[H]) {
         if constexpr (kEl) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (c + 32 * j < width) m[e + 32 * j] = A::down(j & 1 ? v[j / 2].y : v[j / 2].x);
-        } else if (KIND == kFull || (c >= 0 && c + N <= width)) {
-            *reinterpret_cast<uint4 *>(m + e) = U::down(v);
+                if (c + 32 * j < width) m[32 * j] = A::down(j & 1 ? v[j / 2].y : v[j / 2].x);
+        } else if (KIND == kFull || in) {
+            *reinterpret_cast<uint4 *>(m) = U::down(v);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (c + j >= 0 && c + j < width) m[e + j] = A::down(j & 1 ? v[j / 2].y : v[j / 2].x);
+                if ((unsigned)(c + j) < (unsigned)width) m[j] = A::down(j & 1 ? v[j / 2].y : v[j / 2].x);
         }
     };
-    auto store8 = [&](long long e, int c, const float2 (&v)[H]) {
-        uint8_t *m = static_cast<uint8_t *>(p.out) + e;
+    auto store8 = [&](uint8_t *m, int c, bool in, const float2 (&v)[H]) {
         if constexpr (kEl) {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (c + 32 * j < width) m[32 * j] = to_e4m3(j & 1 ? v[j / 2].y : v[j / 2].x);
-        } else if (KIND == kFull || (c >= 0 && c + N <= width)) {
+        } else if (KIND == kFull || in) {
             U::store8(m, v);
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j)
-                if (c + j >= 0 && c + j < width) m[j] = to_e4m3(j & 1 ? v[j / 2].y : v[j / 2].x);
+                if ((unsigned)(c + j) < (unsigned)width) m[j] = to_e4m3(j & 1 ? v[j / 2].y : v[j / 2].x);
         }
     };
-    auto weigh = [&](int c, float2 (&w)[H]) {
-        if constexpr (kShared) {
+    auto weigh = [&](int k, int c, int ph, bool in, float2 (&w)[H]) {  // the weights of unit k
+        if constexpr (kShared && KIND == kFull) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                // the columns of one unit lie in one run of N (kFull), or in two
-                const float f = KIND == kFull || (c + j >= 0 && c + j < width) ? weights[padded<N>(c + j)] : 0.f;
-                (j & 1 ? w[j / 2].y : w[j / 2].x) = f;
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4 *>(weights + c)[i];
+                w[2 * i] = make_float2(v.x, v.y);
+                w[2 * i + 1] = make_float2(v.z, v.w);
             }
-        } else {
-            if (!kEl && !p.weight_f32 && (KIND == kFull || (!(c & (N - 1)) && c + N <= width))) {
+            return;
+        } else if constexpr (kShared) {
+            const float *line = weights + (N - 1 - ph) * kLine + t + k * L;
+#pragma unroll
+            for (int j = 0; j < H; ++j) w[j] = make_float2(line[2 * j * kLine], line[(2 * j + 1) * kLine]);
+            return;
+        }
+        if (!kEl && (KIND == kFull || in)) {
+            if (p.weight_f32) {
+                const float *m = static_cast<const float *>(p.weight) + c;
+                if (KIND == kFull || (c & 3) == 0) {
+#pragma unroll
+                    for (int i = 0; i < N / 4; ++i) {
+                        const float4 v = reinterpret_cast<const float4 *>(m)[i];
+                        w[2 * i] = make_float2(v.x, v.y);
+                        w[2 * i + 1] = make_float2(v.z, v.w);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) w[j] = make_float2(m[2 * j], m[2 * j + 1]);
+                }
+            } else if (KIND == kFull || (c & (N - 1)) == 0) {
                 up(*reinterpret_cast<const uint4 *>(static_cast<const raw *>(p.weight) + c), w);
             } else {
+                const raw *m = static_cast<const raw *>(p.weight) + c;
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int cc = kEl ? c + 32 * j : c + j;
-                    float f;
-                    if constexpr (sizeof(raw) == 2) f = cc >= 0 && cc < width ? weight_at(p, cc, kF16) : 0.f;
-                    else f = cc >= 0 && cc < width ? static_cast<const float *>(p.weight)[cc] : 0.f;
-                    (j & 1 ? w[j / 2].y : w[j / 2].x) = f;
-                }
+                for (int j = 0; j < H; ++j) w[j] = make_float2(A::up(m[2 * j]), A::up(m[2 * j + 1]));
             }
+        } else {
 #pragma unroll
-            for (int j = 0; j < H; ++j) w[j] = fadd2(w[j], make_float2(p.weight_offset, p.weight_offset));
+            for (int j = 0; j < N; ++j) {
+                const int cc = kEl ? c + 32 * j : c + j;
+                const float f = cc >= 0 && cc < width ? weight_at(p, cc, kF16) : 0.f;
+                (j & 1 ? w[j / 2].y : w[j / 2].x) = f;
+            }
         }
+#pragma unroll
+        for (int j = 0; j < H; ++j) w[j] = fadd2(w[j], make_float2(p.weight_offset, p.weight_offset));
     };
 
     // turns of the loop: the same for all threads of a warp; a group without a row left does the last turn on
@@ -270,23 +313,34 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     const int turns = warp_first >= rows ? 0 : (rows - 1 - warp_first) / stride + 1;
     if (kRing) fetch(0, first);
     if (kShared) {
-        for (int c = threadIdx.x; c < width; c += kBlock) weights[padded<N>(c)] = weight_at(p, c, kF16) + p.weight_offset;
+        if (KIND == kFull) {
+            for (int c = threadIdx.x; c < width; c += kBlock) weights[c] = weight_at(p, c, kF16) + p.weight_offset;
+        } else {
+            for (int i = threadIdx.x; i < (2 * N - 1) * kLine; i += kBlock) {
+                const int line = i / kLine, c = (i - line * kLine) * N + line - (N - 1);
+                weights[i] = c >= 0 && c < width ? weight_at(p, c, kF16) + p.weight_offset : 0.f;
+            }
+        }
+    }
+    if (kShared || L > 32) {
+        if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0.f;  // for warps that there are not
         __syncthreads();
     }
     for (int turn = 0; turn < turns; ++turn) {
         const int row = first + turn * stride;
         const bool live = row < rows;
-        const int ph = phase(row);
-        const long long at = (long long)row * width - ph + v0;
+        const int ph = phase(row), c0 = v0 - ph, rest = KIND == kFull ? 0 : rest_of(row);
+        const long long at = (long long)row * width + c0;
+        const raw *rx = x + at, *rr = res + at, *rg = gate + at;
         const uint8_t *held = mine + (turn & 1) * stage_bytes;
         if (kRing) {
             fetch((turn + 1) & 1, row < rows - stride ? row + stride : rows);
             cp_async_wait<1>();
         }
         auto has = [&](int k) {
-            if (KIND == kFull) return live;
-            return live && (kEl ? v0 - (t & 31) + k * kStep < width : v0 + k * kStep - ph < width);
+            return live && (KIND == kFull || (kEl ? c0 - (t & 31) : c0) + k * kStep < width);
         };
+        auto inside = [&](int c) { return KIND == kFull || (c >= 0 && c + N <= width); };
         float2 z[NV][H], sum2 = make_float2(0.f, 0.f);
         constexpr int kBatch = kRing ? 1 : NV / 2;  // units in flight at a time where there is no ring
 #pragma unroll
@@ -295,16 +349,17 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             if (!kRing) {
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int k = k0 + i, c = v0 + k * kStep - ph;
+                    const int k = k0 + i, c = c0 + k * kStep;
                     if (!has(k)) continue;
-                    xw[i] = load(x, at + k * kStep, c);
-                    if (residual) rw[i] = load(res, at + k * kStep, c);
+                    xw[i] = load(rx + k * kStep, c, rest);
+                    if (residual) rw[i] = load(rr + k * kStep, c, rest);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int k = k0 + i, c = v0 + k * kStep - ph;
+                const int k = k0 + i, c = c0 + k * kStep;
                 if (!has(k)) continue;
+                const bool in = inside(c);
                 if (kRing) xw[i] = *reinterpret_cast<const uint4 *>(held + k * kPlane);
                 up(xw[i], z[k]);
                 if (residual) {
@@ -313,9 +368,9 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                     up(rw[i], r);
 #pragma unroll
                     for (int j = 0; j < H; ++j) z[k][j] = fadd2(z[k][j], r[j]);
-                    store(static_cast<raw *>(p.residual_out), at + k * kStep, c, z[k]);
+                    store(static_cast<raw *>(p.residual_out) + at + k * kStep, c, in, z[k]);
                 }
-                mask(c, z[k]);
+                mask(c, in, z[k]);
 #pragma unroll
                 for (int j = 0; j < H; ++j) sum2 = ffma2(z[k][j], z[k][j], sum2);
             }
@@ -331,22 +386,23 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         float most = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int c = v0 + k * kStep - ph;
-            const long long e = at + k * kStep;
+            if (KIND != kFull && k * kStep - (N - 1) >= width) break;  // no thread has such a unit
+            const int c = c0 + k * kStep;
+            const bool in = inside(c);
             float m = 0.f;
             if (has(k)) {
                 float2 w[H];
-                weigh(c, w);
+                weigh(k, c, ph, in, w);
 #pragma unroll
                 for (int j = 0; j < H; ++j) z[k][j] = fmul2(fmul2(z[k][j], make_float2(rstd, rstd)), w[j]);
                 if (gated) {
                     float2 g[H];
-                    up(kRing ? *reinterpret_cast<const uint4 *>(held + gate_at + k * kPlane) : load(gate, e, c), g);
-                    mask(c, g);
+                    up(kRing ? *reinterpret_cast<const uint4 *>(held + gate_at + k * kPlane) : load(rg + k * kStep, c, rest), g);
+                    mask(c, in, g);
 #pragma unroll
                     for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], silu(g[j]));
                 }
-                if (quant == GDN_QUANT_NONE) store(static_cast<raw *>(p.out), e, c, z[k]);
+                if (quant == GDN_QUANT_NONE) store(static_cast<raw *>(p.out) + at + k * kStep, c, in, z[k]);
                 else {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
@@ -362,7 +418,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 if (has(k)) {
 #pragma unroll
                     for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], make_float2(inv, inv));
-                    store8(e, c, z[k]);
+                    store8(static_cast<uint8_t *>(p.out) + at + k * kStep, c, in, z[k]);
                     if ((t & (kGroupLanes - 1)) == 0)
                         p.scales[(long long)row * ((width + GDN_QUANT_GROUP - 1) / GDN_QUANT_GROUP) +
                                  c / GDN_QUANT_GROUP] = scale;
@@ -384,7 +440,8 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 if (!has(k)) continue;
 #pragma unroll
                 for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], make_float2(inv, inv));
-                store8(at + k * kStep, v0 + k * kStep - ph, z[k]);
+                const int c = c0 + k * kStep;
+                store8(static_cast<uint8_t *>(p.out) + at + k * kStep, c, inside(c), z[k]);
             }
         } else if (L > 32) {
             __syncthreads();  // red[0] is read before the next row writes it
@@ -398,8 +455,8 @@ cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
     const auto kern = rms_norm_kernel<A, KIND, L>;
     constexpr int block = norm_block(L), rows = L <= 32 ? block / L : 1;
     const int matrices = 1 + (p.residual != nullptr) + (p.gate != nullptr);
-    size_t smem = norm_ring(KIND, L) ? (size_t)2 * block * 32 * sizeof(typename A::raw) * matrices : 0;
-    if (norm_weights(KIND, L)) smem += (padded<Unit<A>::N>(32 * L) * 4 + 15) / 16 * 16;
+    const size_t smem = norm_weight_bytes<A>(KIND, L) +
+                        (norm_ring<A>(KIND, L) ? (size_t)2 * block * norm_per<A>(L) * sizeof(typename A::raw) * matrices : 0);
     if (smem > 47 * 1024) {  // 48 KB with the static part
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -410,22 +467,13 @@ cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
     return cudaGetLastError();
 }
 
-// The threads of a row: as few as hold `places` places, 32 each, and at least `least`.
-template <class A, Kind KIND>
+// The threads of a row: the fewest of those built that hold `places` places, at least `least`.
+template <class A, Kind KIND, int L, int... MORE>
 cudaError_t launch_lanes(const NormParams &p, int places, int least, cudaStream_t st)
 {
-    const int lanes = std::max(least, (places + 31) / 32);
-    if (KIND != kElements) {
-        if (lanes <= 4) return launch_kernel<A, KIND == kElements ? kFull : KIND, 4>(p, st);
-        if (lanes <= 8) return launch_kernel<A, KIND == kElements ? kFull : KIND, 8>(p, st);
-        if (lanes <= 16) return launch_kernel<A, KIND == kElements ? kFull : KIND, 16>(p, st);
-        if (lanes > 32 && lanes <= 64) return launch_kernel<A, KIND == kElements ? kFull : KIND, 64>(p, st);
-        if (lanes > 128 && lanes <= 256) return launch_kernel<A, KIND == kElements ? kFull : KIND, 256>(p, st);
-    }
-    if (lanes <= 32) return launch_kernel<A, KIND, 32>(p, st);
-    if (lanes <= 128) return launch_kernel<A, KIND, 128>(p, st);
-    if (lanes <= 512) return launch_kernel<A, KIND, 512>(p, st);
-    return launch_kernel<A, KIND, 1024>(p, st);
+    if constexpr (sizeof...(MORE) > 0)
+        if (L < least || L * norm_per<A>(L) < places) return launch_lanes<A, KIND, MORE...>(p, places, least, st);
+    return launch_kernel<A, KIND, L>(p, st);
 }
 
 template <class A>
@@ -436,13 +484,15 @@ cudaError_t launch_type(NormParams p, cudaStream_t st)
     if (p.quant == GDN_QUANT_BLOCK && width <= GDN_QUANT_GROUP) p.quant = GDN_QUANT_ROW;  // one group a row
     const int least = p.quant == GDN_QUANT_BLOCK ? 128 / N : 0;  // lanes that hold a group
     if (width % N == 0) {
-        const bool full = width >= 128 && width <= 32768 && (width & (width - 1)) == 0 && width / 32 >= least;
-        return full ? launch_lanes<A, kFull>(p, width, least, st) : launch_lanes<A, kBlocks>(p, width, least, st);
+        int lanes = std::max(4, least);
+        while (lanes * norm_per<A>(lanes) < width) lanes *= 2;
+        return lanes * norm_per<A>(lanes) == width ? launch_lanes<A, kFull, 4, 8, 16, 32, 64, 128, 256, 512, 1024>(p, width, least, st)
+                    : launch_lanes<A, kBlocks, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width, least, st);
     }
-    if (p.quant == GDN_QUANT_BLOCK) return launch_lanes<A, kElements>(p, width, 0, st);
+    if (p.quant == GDN_QUANT_BLOCK) return launch_lanes<A, kElements, 32, 128, 512, 1024>(p, width, 0, st);
     // a row that begins inside a block may take a unit more; the widest do not find room for it
-    if (width + N - 1 > GDN_NORM_MAX_WIDTH) return launch_lanes<A, kElements>(p, width, 0, st);
-    return launch_lanes<A, kBlocks>(p, width + N - 1, 0, st);
+    if (width + N - 1 > GDN_NORM_MAX_WIDTH) return launch_lanes<A, kElements, 1024>(p, width, 0, st);
+    return launch_lanes<A, kBlocks, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width + N - 1, 0, st);
 }
 
 }  // namespace
