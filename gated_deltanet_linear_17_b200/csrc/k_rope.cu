@@ -6,14 +6,21 @@
 // for the columns (i, n + i) of the first 2 n of a head, or (2 i, 2 i + 1) when interleaved.  Three
 // multiplications an element against 4 bytes moved: HBM bounds it.  One launch does q, k, v and both
 // cache writes, so every row is read once and written once, and the angles of a token are computed
-// once for all its heads (into shared memory, then read by every row of the CTA's tokens).
+// once for all its heads.
 //
 // The angle.  position * inv_freq has up to 55 significant bits; fp32 would leave an error of
 // position * 2^-24 radians.  It is formed in fp64 and reduced by k 2 pi with 2 pi in two parts, so the
-// reduced angle is good to about 1e-15 * k before its rounding to fp32.
+// reduced angle is good to about 1e-15 * k before its rounding to fp32 (2^-23 at most); the fast sine and
+// cosine are then within 2^-21.2 of the exact ones, below a sixteenth of fp16's rounding of a turned element.
 //
-// Work is cut into units of 8 columns (16 when the unit is a pair of 8-column runs, as in the half
-// layout): a thread reads its whole unit before it writes it, so q_out may be q.
+// Layout.  A lane holds 8 neighbouring columns, a row (one head of q, k or v) lies in D / 8 lanes of one
+// warp, and a lane keeps its columns for all rows of its token: its cosines and signed sines, eight of each,
+// stay in registers, y_j = x_j c_j + partner_j s_j.  The partner of a column lies in the same lane
+// (interleaved), in the lane n / 8 away (shuffles), or, when n is no multiple of 8, across two lanes (read
+// again, from L1).  A warp takes as many tokens as it has room for rows, and reads up to four heads ahead of its
+// work on them; where there are few tokens, several warps share their heads.
+#include <algorithm>
+
 #include "gdn_layers.h"
 #include "layers.cuh"
 
@@ -21,159 +28,172 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32, kAhead = 4;
+enum Layout { kPairs, kHalves, kHalvesUnaligned };
 
-// sin and cos of position * f, f fp32
+// mscale times the cosine and sine of position * f
 __device__ __forceinline__ float2 turn(int position, float f, float mscale)
 {
     constexpr double kTwoPiHi = 6.283185307179586, kTwoPiLo = 2.4492935982947064e-16, kInv = 0.15915494309189535;
     const double x = (double)position * (double)f;
     const double k = rint(x * kInv);
-    const double r = fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, x));
-    float s, c;
-    sincosf((float)r, &s, &c);
-    return make_float2(c * mscale, s * mscale);
+    const float r = (float)fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, x));
+    return make_float2(__cosf(r) * mscale, __sinf(r) * mscale);
 }
 
-template <class A>
-__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float2 *cs)
-{
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float c = cs[j].x, s = cs[j].y, x = a[j], y = b[j];
-        a[j] = x * c - y * s;
-        b[j] = y * c + x * s;
-    }
-}
+// CTAs an SM that the registers are cut for: three where nothing is spilled for it
+constexpr int rope_ctas(int size, Layout layout, int dim) { return size == 4 || layout == kHalvesUnaligned || dim == 0 ? 2 : 3; }
 
-// one unit of a turned head (row: its D elements): u counts the head's units
-template <class A, bool INTERLEAVED>
-__device__ __forceinline__ void turn_unit(const typename A::raw *src, typename A::raw *dst, typename A::raw *dst2,
-                                          int u, int n, int D, const float2 *cs)
+// DIM: the head dimension, or 0 for any other than those built
+template <class A, Layout LAYOUT, int DIM>
+__global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(typename A::raw), LAYOUT, DIM))
+    rope_kernel(const RopeParams p)
 {
     using raw = typename A::raw;
-    if (INTERLEAVED) {
-        const int c = 8 * u;
-        Raw8<A> r;
-        r.load(src + c);
-        if (c < 2 * n) {
-            float x[8];
-            r.up(x);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (c / 2 + j >= n) break;
-                const float2 t = cs[c / 2 + j];
-                const float a = x[2 * j], b = x[2 * j + 1];
-                x[2 * j] = a * t.x - b * t.y;
-                x[2 * j + 1] = b * t.x + a * t.y;
-            }
-            r.down(x);
-        }
-        if (dst) r.store(dst + c);
-        if (dst2) r.store(dst2 + c);
-        return;
-    }
-    const int pairs = (n + 7) >> 3;
-    if (u < pairs) {
-        const int i = 8 * u;
-        if ((n & 7) == 0) {
-            Raw8<A> ra, rb;
-            ra.load(src + i);
-            rb.load(src + n + i);
-            float a[8], b[8];
-            ra.up(a);
-            rb.up(b);
-            turn8<A>(a, b, cs + i);
-            ra.down(a);
-            rb.down(b);
-            if (dst) ra.store(dst + i), rb.store(dst + n + i);
-            if (dst2) ra.store(dst2 + i), rb.store(dst2 + n + i);
-        } else {
-            const int m = min(8, n - i);
-            for (int j = 0; j < m; ++j) {
-                const float a = A::up(src[i + j]), b = A::up(src[n + i + j]);
-                const float2 t = cs[i + j];
-                const raw x = A::down(a * t.x - b * t.y), y = A::down(b * t.x + a * t.y);
-                if (dst) dst[i + j] = x, dst[n + i + j] = y;
-                if (dst2) dst2[i + j] = x, dst2[n + i + j] = y;
-            }
-        }
-        return;
-    }
-    // the columns that pass unchanged, from 2 n on: 8-column runs of the head, the first perhaps partial
-    const int c0 = max(2 * n, 8 * ((2 * n >> 3) + u - pairs)), c1 = 8 * ((2 * n >> 3) + u - pairs + 1);
-    if (c1 - c0 == 8) {
-        Raw8<A> r;
-        r.load(src + c0);
-        if (dst && dst != src) r.store(dst + c0);
-        if (dst2) r.store(dst2 + c0);
-    } else {
-        for (int c = c0; c < c1; ++c) {
-            const raw x = src[c];
-            if (dst) dst[c] = x;
-            if (dst2) dst2[c] = x;
-        }
-    }
-}
+    extern __shared__ __align__(16) float2 angles[];  // [tokens of the CTA][n, rounded up to an even number]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int D = DIM ? DIM : p.D, n = p.n, pitch = (n + 1) & ~1;
+    const int lanes = D / 8, per = 32 / lanes;  // lanes a row, tokens a warp
+    const int sub = lane / lanes, c = 8 * (lane - sub * lanes);
+    const int split = p.split, tokens = kRopeWarps / split * per;  // warps that share their tokens' heads, tokens a CTA
+    const long long t0 = (long long)blockIdx.x * tokens;
+    const int mine = warp / split * per + sub, first_row = warp % split, step = split;  // token of the CTA; its heads
+    const long long t = t0 + mine;
+    const bool live = sub < per && t < p.T;
+    const int at0 = first_row * D + c, jump = step * D;
 
-template <class A, bool INTERLEAVED>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p)
-{
-    using raw = typename A::raw;
-    extern __shared__ float2 cs[];  // [tokens_per_cta][n]
-    const long long t0 = (long long)blockIdx.x * p.tokens_per_cta;
-    const int tokens = (int)min((long long)p.tokens_per_cta, p.T - t0);
-    for (int i = threadIdx.x; i < tokens * p.n; i += kRopeThreads) {
-        const int t = i / p.n;
-        cs[i] = turn(p.positions[t0 + t], p.inv_freq[i - t * p.n], p.mscale);
+    const raw *q = static_cast<const raw *>(p.q) + t * p.Hq * D + at0;
+    Raw8<A> ahead[kAhead];
+    auto read = [&](const raw *src, int i0, int rows) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (live && first_row + (i0 + i) * step < rows) ahead[i].load(src + (i0 + i) * jump);
+    };
+    read(q, 0, p.Hq);
+    long long slot = -1;
+    if (p.slots && live) {
+        slot = p.slots[t];
+        if (slot >= p.cache_rows) slot = -1;
+    }
+
+    const int here = (int)min((long long)tokens, p.T - t0) * n;
+    for (int i = threadIdx.x; i < here; i += kRopeThreads) {
+        const int tt = i / n, j = i - tt * n;
+        angles[tt * pitch + j] = turn(p.positions[t0 + tt], p.inv_freq[j], p.mscale);
     }
     __syncthreads();
-    const int total = tokens * p.token_units;
-    const int q_units = p.Hq * p.head_units, k_units = p.Hkv * p.head_units;
-    for (int i = threadIdx.x; i < total; i += kRopeThreads) {
-        const int tt = (int)fast_div(i, p.by_token);
-        int r = i - tt * p.token_units;
-        const long long t = t0 + tt;
-        const float2 *angles = cs + tt * p.n;
-        if (r < q_units) {
-            const int h = (int)fast_div(r, p.by_head);
-            const long long at = (t * p.Hq + h) * p.D;
-            turn_unit<A, INTERLEAVED>(static_cast<const raw *>(p.q) + at, static_cast<raw *>(p.q_out) + at, nullptr,
-                                      r - h * p.head_units, p.n, p.D, angles);
-            continue;
+
+    // this lane's factors; `kept`: its columns that pass unchanged, a bit each
+    float2 cs[4], sn[4];
+    uint32_t kept = 0;
+    const bool turns = c < 2 * n;
+    if (turns && live) {
+        const float2 *a = angles + mine * pitch;
+        if (LAYOUT == kHalves) {
+            const float4 *f = reinterpret_cast<const float4 *>(a + (c < n ? c : c - n));
+            const float2 sign = c < n ? make_float2(-1.f, -1.f) : make_float2(1.f, 1.f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 v = f[j];
+                cs[j] = make_float2(v.x, v.z);
+                sn[j] = fmul2(make_float2(v.y, v.w), sign);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int cc = c + j;
+                float2 f = make_float2(1.f, 0.f);
+                if (cc >= 2 * n) kept |= 1u << j;
+                else if (LAYOUT == kPairs) f = a[cc / 2];
+                else f = a[cc < n ? cc : cc - n];
+                const bool minus = LAYOUT == kPairs ? !(j & 1) : cc < n;
+                (j & 1 ? cs[j / 2].y : cs[j / 2].x) = f.x;
+                (j & 1 ? sn[j / 2].y : sn[j / 2].x) = minus ? -f.y : f.y;
+            }
         }
-        r -= q_units;
-        long long slot = -1;
-        if (p.slots) {
-            slot = p.slots[t];
-            if (slot >= p.cache_rows) slot = -1;
-        }
-        if (r < k_units) {
-            const int h = (int)fast_div(r, p.by_head);
-            const long long at = (t * p.Hkv + h) * p.D;
-            raw *out = p.k_out ? static_cast<raw *>(p.k_out) + at : nullptr;
-            raw *row = slot >= 0 ? static_cast<raw *>(p.k_cache) + (slot * p.Hkv + h) * p.D : nullptr;
-            if (out || row)
-                turn_unit<A, INTERLEAVED>(static_cast<const raw *>(p.k) + at, out, row, r - h * p.head_units, p.n,
-                                          p.D, angles);
-            continue;
-        }
-        r -= k_units;
-        if (slot < 0) continue;
-        Raw8<A> x;
-        x.load(static_cast<const raw *>(p.v) + t * p.Hkv * p.D + 8 * r);
-        x.store(static_cast<raw *>(p.v_cache) + slot * p.Hkv * p.D + 8 * r);
     }
+    const int reach = n / 8, from = !turns ? lane : c < n ? lane + reach : lane - reach;  // kHalves: the partner's lane
+
+    // one row that lies at src, from its 8 columns x here
+    auto turned = [&](Raw8<A> &x, const raw *src) {
+        Raw8<A> other;
+        if (LAYOUT == kHalves) other = x.shuffled(from);
+        if (live && turns) {
+            float2 own[4], with[4];
+            x.up2(own);
+            if (LAYOUT == kPairs) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) with[j] = make_float2(own[j].y, own[j].x);
+            } else if (LAYOUT == kHalves) {
+                other.up2(with);
+            } else {
+                float f[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = c + j < 2 * n ? A::up(src[c + j < n ? j + n : j - n]) : 0.f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) with[j] = make_float2(f[2 * j], f[2 * j + 1]);
+            }
+            float2 z[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                z[j] = ffma2(with[j], sn[j], fmul2(own[j], cs[j]));
+                if (LAYOUT != kHalves) {
+                    if (kept >> (2 * j) & 1) z[j].x = own[j].x;
+                    if (kept >> (2 * j + 1) & 1) z[j].y = own[j].y;
+                }
+            }
+            x.down2(z);
+        }
+        if (LAYOUT == kHalvesUnaligned) __syncwarp();  // q_out may be q: the partners are read before the writes
+    };
+    // the rows of one kind: `ahead` holds the first kAhead of them
+    auto rows_of = [&](const raw *src, raw *out, raw *cached, int rows, bool turn) {
+        for (int i0 = 0; first_row + i0 * step < rows; i0 += kAhead) {
+            Raw8<A> x[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) x[i] = ahead[i];
+            if (first_row + (i0 + kAhead) * step < rows) read(src, i0 + kAhead, rows);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                if (first_row + (i0 + i) * step >= rows) break;  // the whole warp is done
+                if (turn) turned(x[i], src + (i0 + i) * jump);
+                if (live && out) x[i].store(out + (i0 + i) * jump);
+                if (live && cached) x[i].store(cached + (i0 + i) * jump);
+            }
+        }
+    };
+    rows_of(q, static_cast<raw *>(p.q_out) + t * p.Hq * D + at0, nullptr, p.Hq, true);
+    const long long kv = t * p.Hkv * D + at0, row = slot * p.Hkv * D + at0;
+    raw *k_out = p.k_out ? static_cast<raw *>(p.k_out) + kv : nullptr;
+    raw *k_row = slot >= 0 ? static_cast<raw *>(p.k_cache) + row : nullptr;
+    read(static_cast<const raw *>(p.k) + kv, 0, p.Hkv);
+    rows_of(static_cast<const raw *>(p.k) + kv, k_out, k_row, p.Hkv, true);
+    if (slot >= 0) {
+        read(static_cast<const raw *>(p.v) + kv, 0, p.Hkv);
+        rows_of(static_cast<const raw *>(p.v) + kv, nullptr, static_cast<raw *>(p.v_cache) + row, p.Hkv, false);
+    }
+}
+
+template <class A, Layout LAYOUT>
+cudaError_t launch_dim(const RopeParams &p, cudaStream_t st)
+{
+    const int tokens = kRopeWarps / p.split * (32 / (p.D / 8));
+    const unsigned grid = (unsigned)((p.T + tokens - 1) / tokens);
+    const size_t smem = sizeof(float2) * tokens * ((p.n + 1) & ~1);
+    switch (p.D) {
+    case 64: rope_kernel<A, LAYOUT, 64><<<grid, kRopeThreads, smem, st>>>(p); break;
+    case 128: rope_kernel<A, LAYOUT, 128><<<grid, kRopeThreads, smem, st>>>(p); break;
+    case 256: rope_kernel<A, LAYOUT, 256><<<grid, kRopeThreads, smem, st>>>(p); break;
+    default: rope_kernel<A, LAYOUT, 0><<<grid, kRopeThreads, smem, st>>>(p); break;
+    }
+    return cudaGetLastError();
 }
 
 template <class A>
 cudaError_t launch_type(const RopeParams &p, bool interleaved, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((p.T + p.tokens_per_cta - 1) / p.tokens_per_cta);
-    const size_t smem = sizeof(float2) * p.tokens_per_cta * p.n;
-    if (interleaved) rope_kernel<A, true><<<grid, kRopeThreads, smem, st>>>(p);
-    else rope_kernel<A, false><<<grid, kRopeThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    if (interleaved) return launch_dim<A, kPairs>(p, st);
+    return p.n % 8 == 0 ? launch_dim<A, kHalves>(p, st) : launch_dim<A, kHalvesUnaligned>(p, st);
 }
 
 }  // namespace
@@ -181,16 +201,10 @@ cudaError_t launch_type(const RopeParams &p, bool interleaved, cudaStream_t st)
 cudaError_t launch_rope(const RopeParams &in, int act_dtype, bool interleaved, cudaStream_t st)
 {
     RopeParams p = in;
-    p.head_units = interleaved ? p.D / 8 : (p.n + 7) / 8 + p.D / 8 - (2 * p.n >> 3);
-    const int copied = p.k_cache ? p.Hkv * p.D / 8 : 0;
-    p.token_units = (p.Hq + p.Hkv) * p.head_units + copied;
-    // about four units a thread; the angles of a CTA's tokens stay within 16 KB of shared memory
-    long long tokens = 4 * kRopeThreads / p.token_units;
-    const long long most = p.n ? 16384 / (8 * p.n) : tokens;
-    tokens = tokens < 1 ? 1 : tokens > most ? most : tokens;
-    p.tokens_per_cta = (int)(tokens > p.T ? p.T : tokens);
-    p.by_token = FastDiv(p.token_units);
-    p.by_head = FastDiv(p.head_units);
+    // split the heads over warps until the warps fill the GPU (148 SMs of three CTAs)
+    const int heads = std::max(p.Hq, p.Hkv), per = 32 / (p.D / 8);
+    p.split = 1;
+    while (p.split < kRopeWarps && p.split < heads && (p.T + per - 1) / per * p.split < 148 * 3 * kRopeWarps) p.split *= 2;
     switch (act_dtype) {
     case GDN_DTYPE_BF16: return launch_type<Bf16>(p, interleaved, st);
     case GDN_DTYPE_FP16: return launch_type<F16>(p, interleaved, st);

@@ -35,15 +35,15 @@ struct Raw8 {
     uint4 w;
     __device__ __forceinline__ void load(const typename A::raw *p) { w = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void store(typename A::raw *p) const { *reinterpret_cast<uint4 *>(p) = w; }
-    __device__ __forceinline__ void up(float (&x)[8]) const
+    // the 8 elements that lane `from` holds
+    __device__ __forceinline__ Raw8 shuffled(int from) const
     {
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = A::up2(v[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
+        Raw8 r;
+        r.w.x = __shfl_sync(0xffffffffu, w.x, from);
+        r.w.y = __shfl_sync(0xffffffffu, w.y, from);
+        r.w.z = __shfl_sync(0xffffffffu, w.z, from);
+        r.w.w = __shfl_sync(0xffffffffu, w.w, from);
+        return r;
     }
     __device__ __forceinline__ void up2(float2 (&x)[4]) const
     {
@@ -53,10 +53,6 @@ struct Raw8 {
     {
         w = make_uint4(A::down2(x[0].x, x[0].y), A::down2(x[1].x, x[1].y), A::down2(x[2].x, x[2].y),
                        A::down2(x[3].x, x[3].y));
-    }
-    __device__ __forceinline__ void down(const float (&x)[8])
-    {
-        w = make_uint4(A::down2(x[0], x[1]), A::down2(x[2], x[3]), A::down2(x[4], x[5]), A::down2(x[6], x[7]));
     }
 };
 template <>
@@ -72,9 +68,14 @@ struct Raw8<F32> {
         reinterpret_cast<float4 *>(p)[0] = a;
         reinterpret_cast<float4 *>(p)[1] = b;
     }
-    __device__ __forceinline__ void up(float (&x)[8]) const
+    __device__ __forceinline__ Raw8 shuffled(int from) const
     {
-        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+        Raw8 r;
+        r.a.x = __shfl_sync(0xffffffffu, a.x, from), r.a.y = __shfl_sync(0xffffffffu, a.y, from);
+        r.a.z = __shfl_sync(0xffffffffu, a.z, from), r.a.w = __shfl_sync(0xffffffffu, a.w, from);
+        r.b.x = __shfl_sync(0xffffffffu, b.x, from), r.b.y = __shfl_sync(0xffffffffu, b.y, from);
+        r.b.z = __shfl_sync(0xffffffffu, b.z, from), r.b.w = __shfl_sync(0xffffffffu, b.w, from);
+        return r;
     }
     __device__ __forceinline__ void up2(float2 (&x)[4]) const
     {
@@ -85,11 +86,6 @@ struct Raw8<F32> {
     {
         a = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
         b = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
-    }
-    __device__ __forceinline__ void down(const float (&x)[8])
-    {
-        a = make_float4(x[0], x[1], x[2], x[3]);
-        b = make_float4(x[4], x[5], x[6], x[7]);
     }
 };
 

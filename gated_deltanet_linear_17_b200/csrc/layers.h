@@ -45,9 +45,7 @@ struct RopeParams {
     float mscale;
     long long T, cache_rows;
     int Hq, Hkv, D, n;  // n = rotary / 2 angles
-    // filled by the launcher: units of 8 or 16 elements per turned head, per copied head, per token
-    int head_units, token_units, tokens_per_cta;
-    FastDiv by_token, by_head, by_copy;
+    int split;          // warps that share a token (set by the launcher)
 };
 cudaError_t launch_rope(const RopeParams &p, int act_dtype, bool interleaved, cudaStream_t st);
 

@@ -35,7 +35,7 @@ extern "C" {
 #define GDN_QUANT_BLOCK 2 /* out in e4m3, one fp32 scale per row and GDN_QUANT_GROUP columns */
 #define GDN_QUANT_GROUP 128
 #define GDN_NORM_MAX_WIDTH 32768
-#define GDN_ROPE_MAX_DIM 512
+#define GDN_ROPE_MAX_DIM 256
 
 /*
  * gdn_rms_norm -- root-mean-square norm of each row.
@@ -105,7 +105,7 @@ int gdn_rms_norm(const void *x, const void *residual, const void *gate, const vo
  *                 GDN_ROPE_MAX_DIM; rotary even, 0 .. D
  * Alignment: 16 bytes for q, k, v, q_out, k_out and the caches, 4 for the rest.
  * Errors: GDN_ERR_NULL_ARG, GDN_ERR_BAD_SHAPE, GDN_ERR_UNSUPPORTED (D, T >= 2^31,
- * T (Hq + 2 Hkv) >= 2^31, cache_rows >= 2^31), GDN_ERR_ALIGNMENT, GDN_ERR_OVERLAP, GDN_ERR_CUDA.
+ * cache_rows >= 2^31, more than 65535 heads), GDN_ERR_ALIGNMENT, GDN_ERR_OVERLAP, GDN_ERR_CUDA.
  */
 int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *positions, const float *inv_freq,
                  const int32_t *slots, float mscale, void *q_out, void *k_out, void *k_cache, void *v_cache,

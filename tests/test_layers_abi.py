@@ -94,7 +94,7 @@ CACHE = dict(v=7 * M, slots=8 * M, kc=9 * M, vc=10 * M, rows=64, k_out=None)
     (dict(rotary=-2), B.GDN_ERR_BAD_SHAPE),
     (dict(act=7), B.GDN_ERR_BAD_SHAPE),
     (dict(D=60), B.GDN_ERR_UNSUPPORTED),
-    (dict(D=520), B.GDN_ERR_UNSUPPORTED),
+    (dict(D=264), B.GDN_ERR_UNSUPPORTED),
     (dict(T=1 << 31), B.GDN_ERR_UNSUPPORTED),
     (dict(CACHE, rows=1 << 31), B.GDN_ERR_UNSUPPORTED),
     (dict(T=0), B.GDN_OK),
