@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -57,35 +58,21 @@ def _need(t, name, dtype, shape, dev):
 
 @contextlib.contextmanager
 def _on(dev, stream):
-    with torch.cuda.device(dev):
-        if stream is None:
-            yield torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if stream.device != dev:
-                raise RuntimeError(f"the stream is on {stream.device}, the tensors on {dev}")
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+    """``dev`` and ``stream`` (or the device's current stream) as the current ones."""
+    if stream is not None and stream.device != dev:
+        raise RuntimeError(f"the stream is on {stream.device}, the tensors on {dev}")
+    with torch.cuda.device(dev), torch.cuda.stream(stream):
+        yield
 
 
-class _Here:
-    """``_on`` for the common call (the current device, its current stream), without the context's cost."""
-
-    def __init__(self, handle):
-        self.handle = handle
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        return False
+def _elsewhere(dev, stream):
+    """Whether a call on ``dev`` and ``stream`` has to change the current device or stream first."""
+    return stream is not None or dev.index != torch.cuda.current_device()
 
 
-def _place(dev, stream):
-    """Context of a call on ``dev``: the handle of the stream that it runs on, with torch's current stream set to it."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        # the handle itself, a tenth of a microsecond against three for a Stream object
-        return _Here(torch._C._cuda_getCurrentRawStream(dev.index))
-    return _on(dev, stream)
+def _stream_of(dev):
+    # the handle alone: a tenth of a microsecond against more than one for a Stream object
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _cuda(t, name):
@@ -115,6 +102,9 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
     ``out`` may be x (without ``quant``) and ``residual_out`` may be the residual: then they are
     updated in place."""
     act = _act(x, "x")
+    if _elsewhere(x.device, stream):
+        with _on(x.device, stream):
+            return rms_norm(x, weight, residual, gate, eps, weight_offset, quant, out, residual_out, scales)
     if quant not in QUANT:
         raise ValueError(f"quant must be one of {list(QUANT)} (got {quant!r})")
     if x.dim() < 1 or x.shape[-1] < 1:
@@ -142,16 +132,15 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
         if quant is None:
             raise ValueError("scales need quant")
         _need(scales, "scales", torch.float32, sshape, dev)
-    with _place(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(x) if quant is None else torch.empty_like(x, dtype=odt)
-        if residual is not None and residual_out is None:
-            residual_out = torch.empty_like(x)
-        if quant is not None and scales is None:
-            scales = x.new_empty(sshape, dtype=torch.float32)
-        rc = _layers_lib().gdn_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), float(eps),
-                                        float(weight_offset), _ptr(out), _ptr(residual_out), _ptr(scales),
-                                        x.numel() // width, width, _b.DTYPES[act], _b.DTYPES[wdt], QUANT[quant], st)
+    if out is None:
+        out = torch.empty_like(x) if quant is None else torch.empty_like(x, dtype=odt)
+    if residual is not None and residual_out is None:
+        residual_out = torch.empty_like(x)
+    if quant is not None and scales is None:
+        scales = x.new_empty(sshape, dtype=torch.float32)
+    rc = _layers_lib().gdn_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), eps, weight_offset, _ptr(out),
+                                    _ptr(residual_out), _ptr(scales), x.numel() // width, width, _b.DTYPES[act],
+                                    _b.DTYPES[wdt], QUANT[quant], _stream_of(dev))
     _b._check(rc, "gdn_rms_norm")
     return out, residual_out, scales
 
@@ -204,6 +193,9 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     outside the cache marks a padding token, which is not written; slots have to differ), and the turned
     keys are returned only if ``k_out`` is given (else None).  ``q_out`` may be q, ``k_out`` may be k."""
     act = _act(q, "q")
+    if _elsewhere(q.device, stream):
+        with _on(q.device, stream):
+            return rope_fwd(q, k, positions, inv_freq, v, k_cache, v_cache, slots, interleaved, mscale, q_out, k_out)
     if q.dim() != 3:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     _cuda(k, "k")
@@ -236,19 +228,19 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
         _need(q_out, "q_out", act, (T, Hq, D), dev)
     if k_out is not None:
         _need(k_out, "k_out", act, (T, Hkv, D), dev)
-    with _place(dev, stream) as st:
-        if q_out is None:
-            q_out = torch.empty_like(q)
-        if k_out is None and k_cache is None:
-            k_out = torch.empty_like(k)
-        rc = _layers_lib().gdn_rope_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(slots),
-                                        float(mscale), _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), T, Hq,
-                                        Hkv, D, 2 * inv_freq.shape[0], int(bool(interleaved)), rows, _b.DTYPES[act],
-                                        st)
+    if q_out is None:
+        q_out = torch.empty_like(q)
+    if k_out is None and k_cache is None:
+        k_out = torch.empty_like(k)
+    rc = _layers_lib().gdn_rope_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(slots), mscale,
+                                    _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D,
+                                    2 * inv_freq.shape[0], 1 if interleaved else 0, rows, _b.DTYPES[act],
+                                    _stream_of(dev))
     _b._check(rc, "gdn_rope_fwd")
     return q_out, k_out
 
 
+@functools.lru_cache(maxsize=1024)
 def paged_attn_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, max_seqlen=0) -> int:
     """Bytes of workspace of ``paged_attn_fwd`` for these sizes (``gdn_paged_attn_workspace_bytes``)."""
     return int(_layers_lib().gdn_paged_attn_workspace_bytes(B, Hq, Hkv, D, page_size, max_pages, max_seqlen))
@@ -269,6 +261,10 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     of ``paged_attn_workspace_bytes`` bytes, allocated here when not given; calls that can overlap on
     the GPU, replayed graphs among them, need buffers of their own."""
     act = _act(q, "q", (torch.bfloat16, torch.float16))
+    if _elsewhere(q.device, stream):
+        with _on(q.device, stream):
+            return paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, max_seqlen, out, lse, output_lse,
+                                  workspace)
     _cuda(k_cache, "k_cache")
     _cuda(block_table, "block_table")
     if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
@@ -280,6 +276,7 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
         raise ValueError(f"Hq ({Hq}) must be a multiple of Hkv ({Hkv})")
     if page < 1:
         raise ValueError("page_size must be at least 1")
+    max_seqlen = int(max_seqlen)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
     max_pages = block_table.shape[1]
@@ -296,20 +293,18 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
         _cuda(workspace, "workspace")
         if workspace.device != dev or not workspace.is_contiguous():
             raise RuntimeError(f"workspace must be a contiguous tensor on {dev}")
-    with _place(dev, stream) as st:
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None and output_lse:
-            lse = q.new_empty((B, Hq), dtype=torch.float32)
-        if workspace is None:
-            nbytes = paged_attn_workspace_bytes(B, Hq, Hkv, D, page, max_pages, int(max_seqlen))
-            if nbytes:
-                workspace = q.new_empty((nbytes,), dtype=torch.uint8)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        sc = 0.0 if scale is None else float(scale)
-        rc = _layers_lib().gdn_paged_attn_fwd(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                              _ptr(seq_lens), sc, _ptr(out), _ptr(lse), B, Hq, Hkv, D, P, page,
-                                              max_pages, int(max_seqlen), _b.DTYPES[act], _ptr(workspace), ws_bytes,
-                                              st)
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None and output_lse:
+        lse = q.new_empty((B, Hq), dtype=torch.float32)
+    if workspace is None:
+        nbytes = paged_attn_workspace_bytes(B, Hq, Hkv, D, page, max_pages, max_seqlen)
+        if nbytes:
+            workspace = q.new_empty((nbytes,), dtype=torch.uint8)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    rc = _layers_lib().gdn_paged_attn_fwd(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+                                          0.0 if scale is None else scale, _ptr(out), _ptr(lse), B, Hq, Hkv, D, P,
+                                          page, max_pages, max_seqlen, _b.DTYPES[act], _ptr(workspace), ws_bytes,
+                                          _stream_of(dev))
     _b._check(rc, "gdn_paged_attn_fwd")
     return out, lse

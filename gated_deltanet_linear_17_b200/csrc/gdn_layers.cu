@@ -53,10 +53,10 @@ int attn_sizes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
     return GDN_OK;
 }
 
-// workspace of `ctas` CTAs: begun, part_ml, part (one CTA finishes everything itself)
-size_t attn_bytes(int ctas, int32_t D)
+// workspace of a plan's CTAs: begun, part_ml, part (none where clusters finish what they begin)
+size_t attn_bytes(const gdn::AttnPlan &plan, int32_t D)
 {
-    return ctas == 1 ? 0 : (size_t)ctas * (sizeof(int4) + 32 * sizeof(float2) + 32 * D * sizeof(float));
+    return (size_t)plan.ctas * (sizeof(int4) + 32 * sizeof(float2) + 32 * D * sizeof(float));
 }
 
 }  // namespace
@@ -142,7 +142,7 @@ size_t gdn_paged_attn_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_
 {
     int64_t max_len = 0;
     if (attn_sizes(B, Hq, Hkv, D, page_size, max_pages, max_seqlen, &max_len) || B == 0) return 0;
-    return attn_bytes(gdn::attn_ctas(B, Hq, Hkv, D, max_len), D);
+    return attn_bytes(gdn::attn_plan(B, Hq, Hkv, D, max_len), D);
 }
 
 int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, const int32_t *block_table,
@@ -162,8 +162,8 @@ int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, 
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(workspace, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4))
         return GDN_ERR_ALIGNMENT;
-    const int ctas = gdn::attn_ctas(B, Hq, Hkv, D, max_len);
-    const size_t need = attn_bytes(ctas, D);
+    const gdn::AttnPlan plan = gdn::attn_plan(B, Hq, Hkv, D, max_len);
+    const size_t need = attn_bytes(plan, D);
     if (workspace && workspace_bytes < need) return GDN_ERR_WORKSPACE;
     const size_t nq = (size_t)B * Hq * D * 2, nc = (size_t)P * page_size * Hkv * D * 2;
     const Span outs[3] = {{out, nq}, {lse, (size_t)B * Hq * 4}, {workspace, need}};
@@ -179,11 +179,11 @@ int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, 
     gdn::AttnParams p;
     p.q = q, p.k = k_cache, p.v = v_cache, p.table = block_table, p.lens = seq_lens, p.out = out, p.lse = lse;
     p.begun = static_cast<int4 *>(workspace);
-    p.part_ml = reinterpret_cast<float2 *>(p.begun + ctas);
-    p.part = reinterpret_cast<float *>(p.part_ml + 32 * (size_t)ctas);
+    p.part_ml = reinterpret_cast<float2 *>(p.begun + plan.ctas);
+    p.part = reinterpret_cast<float *>(p.part_ml + 32 * (size_t)plan.ctas);
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.44269504f;
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.group = Hq / Hkv, p.row_tiles = (Hq / Hkv + 15) / 16;
-    p.P = P, p.page_size = page_size, p.max_pages = max_pages, p.ctas = ctas;
+    p.P = P, p.page_size = page_size, p.max_pages = max_pages, p.ctas = plan.ctas, p.direct = plan.direct;
     p.by_page = gdn::FastDiv((uint32_t)page_size);
     rc = cuda_status(gdn::launch_paged_attn(p, D, act_dtype == GDN_DTYPE_FP16, st));
     if (own && cudaFreeAsync(own, st) != cudaSuccess && rc == GDN_OK) rc = GDN_ERR_CUDA;

@@ -16,6 +16,10 @@
 // (started early by a programmatic dependency) joins a pair's pieces in their order, so the result does
 // not depend on the order in which CTAs run.
 //
+// Short sequences (attn_direct) do without the list, the workspace and the second kernel: each pair is one
+// cluster's, its keys cut over the cluster's CTAs, which join their results through distributed shared
+// memory.
+//
 // Inside a CTA four warps take every fourth tile of 16 keys.  A warp is on its own until the end of the
 // piece: its own ring of tiles in shared memory, filled by cp.async a few tiles ahead, its own running
 // maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end of a piece the
@@ -38,10 +42,12 @@ namespace {
 constexpr int kTile = 16;  // keys a warp takes at a time
 constexpr float kLn2 = 0.693147181f;
 
-// NT: octets of query rows (1 or 2)
-template <int D, int NT>
+// NT: octets of query rows (1 or 2).  A warp's ring of 256-column tiles takes 48 KB: two CTAs of two warps an SM
+// where the CTAs fill the GPU, one of four where short sequences leave room (DIRECT).
+template <int D, int NT, bool DIRECT>
 struct Shape {
-    static constexpr int kWarps = D == 256 ? 2 : 4, kThreads = 32 * kWarps;
+    static constexpr int kWarps = D == 256 && !DIRECT ? 2 : 4, kThreads = 32 * kWarps;
+    static constexpr int kCtas = DIRECT ? kDirectCtasPerSm(D) : kAttnCtasPerSm(D);
     static constexpr int kStages = D == 64 ? 4 : 3;
     static constexpr int kHalf = kTile * D * 2;      // bytes of a tile's keys (or values)
     static constexpr int kStage = 2 * kHalf;
@@ -153,42 +159,103 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     return found;
 }
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) paged_attn_kernel(const AttnParams p)
+__device__ __forceinline__ void cluster_arrive_wait()
 {
-    using S = Shape<D, NT>;
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
+}
+// the address of shared-memory address a in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t in_cta(uint32_t a, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t a)
+{
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ float2 cluster_load2(uint32_t a)
+{
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+    return v;
+}
+
+// 4 columns from 4 c on of one query head's output, x unnormalised, and its lse
+template <int D, bool F16>
+__device__ __forceinline__ void write_out(const AttnParams &p, long long head, int c, float4 x, float top, float sum)
+{
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + head * D + 4 * c) =
+        make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
+    if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+}
+
+// DIRECT: a cluster of p.direct CTAs a pair
+template <int D, int NT, bool F16, bool DIRECT>
+__global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, DIRECT>::kCtas)
+    paged_attn_kernel(const AttnParams p)
+{
+    using S = Shape<D, NT, DIRECT>;
     constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
-    asm volatile("griddepcontrol.launch_dependents;");
+    __shared__ float2 joined[kRows];  // DIRECT: maximum and sum of this CTA's part of the keys
+    if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const uint32_t qs = smem_addr(smem) + kWarps * S::kRing;
     const uint16_t *kc = static_cast<const uint16_t *>(p.k), *vc = static_cast<const uint16_t *>(p.v);
     const int heads = p.Hkv * p.row_tiles;
 
-    const Part part = find_part<D, kThreads>(p);
-    if ((int)blockIdx.x >= part.ctas) {
-        if (tid == 0) p.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
-        return;
-    }
-    long long left_places = part.total * (blockIdx.x + 1) / part.ctas - part.first;
-    int b = part.b, n_raw = p.lens[b], u_all = places<D>(n_raw, p);
-    int pair = (int)(part.rest / u_all), u0 = (int)(part.rest - (long long)pair * u_all);
-    long long pos = part.first;
+    int b, pair, n_raw;
+    // the list: this CTA's part of it, the places of a pair of sequence b, and the first place of the piece at hand
+    Part part = {};
+    long long left_places = 0, pos = 0;
+    int u_all = 0, u0 = 0;
     int4 begun = make_int4(0, 0, 0, 0);
+    const int rank = DIRECT ? (int)blockIdx.x % p.direct : 0;
+    if (DIRECT) {
+        const int at = (int)blockIdx.x / p.direct;
+        b = at / heads;
+        pair = at - b * heads;
+        n_raw = p.lens[b];
+    } else {
+        part = find_part<D, kThreads>(p);
+        if ((int)blockIdx.x >= part.ctas) {
+            if (tid == 0) p.begun[blockIdx.x] = begun;
+            return;
+        }
+        left_places = part.total * (blockIdx.x + 1) / part.ctas - part.first;
+        pos = part.first;
+        b = part.b;
+        n_raw = p.lens[b];
+        u_all = places<D>(n_raw, p);
+        pair = (int)(part.rest / u_all);
+        u0 = (int)(part.rest - (long long)pair * u_all);
+    }
 
     for (;;) {
-    // this piece: places [u0, u0 + take) of head group `pair` of sequence b
-    const int take = (int)min(left_places, (long long)(u_all - u0));
-    const bool whole = take == u_all;
+    // this piece: keys [k0, k1) of head group `pair` of sequence b; of the list, places [u0, u0 + take)
+    const int take = DIRECT ? 0 : (int)min(left_places, (long long)(u_all - u0));
+    const bool whole = DIRECT ? p.direct == 1 : take == u_all;
     const bool bad = bad_length(n_raw, p);
     const int n = bad ? 0 : n_raw;
     const int hkv = pair / p.row_tiles, tile_row0 = (pair - hkv * p.row_tiles) * kRows;
     const int rows = min(kRows, p.group - tile_row0);
     const int head0 = hkv * p.group + tile_row0;  // first query head of this piece
-    const int k0 = max(0, u0 - kLead<D>) * kAttnUnit, k1 = min(n, max(0, u0 + take - kLead<D>) * kAttnUnit);
-    const int n_next = b + 1 < p.B ? p.lens[b + 1] : 0;
+    int k0, k1;
+    if (DIRECT) {
+        const int each = (n / p.direct + kTile) & ~(kTile - 1);  // above n / direct
+        k0 = min(n, rank * each);
+        k1 = min(n, k0 + each);
+    } else {
+        k0 = max(0, u0 - kLead<D>) * kAttnUnit;
+        k1 = min(n, max(0, u0 + take - kLead<D>) * kAttnUnit);
+    }
+    const int n_next = !DIRECT && b + 1 < p.B ? p.lens[b + 1] : 0;
 
     // this warp's tiles: first + 16 (warp + 4 i)
     const int tiles = (k1 - k0 + kTile - 1) / kTile;
@@ -394,17 +461,50 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, kAttnCtasPerSm(D)) pag
             sum += wl[w][row] * exp2f(wm[w][row] - top);
         }
         if (whole) {
-            const long long at = (long long)b * p.Hq + head0 + row;
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
-                make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-            if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+            write_out<D, F16>(p, (long long)b * p.Hq + head0 + row, c, x, top, sum);
+        } else if (DIRECT) {
+            reinterpret_cast<float4 *>(os + row * S::kSum)[c] = x;  // where this thread read the first warp's part
+            if (c == 0) joined[row] = make_float2(sum == 0.f ? -INFINITY : top, sum);
         } else {
-            // place 1: the pair begins here; place 0: it began in an earlier CTA
+            // place 1: the pair begins here; place 0: it began in an earlier CTA.  A piece without a weight has no
+            // maximum either: its stand-in 0 would drown scores far below it
             const long long at = (2LL * blockIdx.x + (u0 == 0)) * 16 + row;
             reinterpret_cast<float4 *>(p.part + at * D)[c] = x;
-            if (c == 0) p.part_ml[at] = make_float2(top, sum);
+            if (c == 0) p.part_ml[at] = make_float2(sum == 0.f ? -INFINITY : top, sum);
         }
+    }
+    if (DIRECT) {
+        if (whole) return;
+        cluster_arrive_wait();
+        for (int i = rank * kThreads + tid; i < rows * (D / 4); i += p.direct * kThreads) {
+            const int row = i / (D / 4), c = i % (D / 4);
+            const uint32_t ml = smem_addr(joined + row), xs = smem_addr(os + row * S::kSum) + 16 * c;
+            float2 part_ml[kAttnMaxCluster];
+            float4 part_x[kAttnMaxCluster];
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int r = 0; r < kAttnMaxCluster; ++r) {
+                if (r >= p.direct) break;
+                part_ml[r] = cluster_load2(in_cta(ml, r));
+                part_x[r] = cluster_load4(in_cta(xs, r));
+            }
+#pragma unroll
+            for (int r = 0; r < kAttnMaxCluster; ++r)
+                if (r < p.direct) top = fmaxf(top, part_ml[r].x);
+            top = top == -INFINITY ? 0.f : top;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int r = 0; r < kAttnMaxCluster; ++r) {
+                if (r >= p.direct) break;
+                const float w = exp2f(part_ml[r].x - top);
+                sum = fmaf(w, part_ml[r].y, sum);
+                x.x = fmaf(w, part_x[r].x, x.x), x.y = fmaf(w, part_x[r].y, x.y);
+                x.z = fmaf(w, part_x[r].z, x.z), x.w = fmaf(w, part_x[r].w, x.w);
+            }
+            write_out<D, F16>(p, (long long)b * p.Hq + head0 + row, c, x, top, sum);
+        }
+        cluster_arrive_wait();  // no CTA leaves while another reads its shared memory
+        return;
     }
     if (!whole && u0 == 0) {
         // the CTA that holds the pair's last place u: the largest i with floor(i total / ctas) <= u
@@ -479,12 +579,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const Att
         *inner = item - (lo ? (int)(upto[lo - 1] >> shift & 0xffff) : 0);
         return lo;
     };
-    auto write = [&](const int4 &rec, int row, int c, float4 x, float top, float sum) {  // 4 columns from 4 c on
-        const long long at = (long long)rec.x * p.Hq + rec.y + row;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at * D + 4 * c) =
-            make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-        if (p.lse && c == 0) p.lse[at] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+    auto write = [&](const int4 &rec, int row, int c, float4 x, float top, float sum) {
+        write_out<D, F16>(p, (long long)rec.x * p.Hq + rec.y + row, c, x, top, sum);
     };
     auto place = [&](int first, int j, int row) { return (2LL * (first + j) + (j == 0)) * 16 + row; };
 
@@ -568,12 +664,30 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const Att
 template <int D, int NT, bool F16>
 cudaError_t launch(const AttnParams &p, cudaStream_t st)
 {
-    using S = Shape<D, NT>;
-    const auto kern = paged_attn_kernel<D, NT, F16>;
+    if (p.direct) {
+        using S = Shape<D, NT, true>;
+        const auto kern = paged_attn_kernel<D, NT, F16, true>;
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.row_tiles * p.direct));
+        cfg.blockDim = dim3(S::kThreads);
+        cfg.dynamicSmemBytes = S::kSmem;
+        cfg.stream = st;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)p.direct;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, p);
+    }
+    using S = Shape<D, NT, false>;
+    const auto kern = paged_attn_kernel<D, NT, F16, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     kern<<<(unsigned)p.ctas, S::kThreads, S::kSmem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess || p.ctas == 1) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kJoinCtas);
     cfg.blockDim = dim3(kJoinThreads);
@@ -588,11 +702,24 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
 
 }  // namespace
 
-int attn_ctas(int B, int Hq, int Hkv, int D, long long max_len)
+// A cluster a pair where that leaves a CTA at most kDirectKeys keys; measured (us, clusters against the list):
+//   1 sequence of 2 heads, D = 128: 512 keys 5.8 / 8.1, 2048 keys 8.1 / 9.1, 4096 keys (512 a CTA) 11.4 / 9.9
+//   1 sequence of 2 heads, D = 256: 512 keys 8.1 / 13.6, 2048 keys 12.4 / 14.1, 4096 keys 17.3 / 15.1
+//   16 sequences of 8 heads, D = 128: 512 keys (256 a CTA) 9.4 / 13.6, 2048 keys of unequal lengths 19.6 / 20.7
+//   64 sequences of 8 heads (more pairs than CTAs fit at once), D = 128: 256 keys 13 / 18, 2048 keys of unequal
+//   lengths 67 / 56; D = 256, one CTA an SM: 64 keys 15 / 19, 256 keys 40 / 37, hence kDirectKeysQueued there
+constexpr int kDirectKeys = 256, kDirectKeysQueued = 64;
+static_assert(kDirectKeys >= kAttnUnit && kDirectKeysQueued >= kAttnUnit, "a list has two units or more");
+
+AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len)
 {
-    const long long heads = (long long)Hkv * ((Hq / Hkv + 15) / 16);
-    const long long most = (long long)B * heads * std::max(1LL, (max_len + kAttnUnit - 1) / kAttnUnit);
-    return (int)std::min<long long>(most, kAttnSms * kAttnCtasPerSm(D));
+    const long long pairs = (long long)B * Hkv * ((Hq / Hkv + 15) / 16), slots = kAttnSms * kDirectCtasPerSm(D);
+    int cluster = 1;
+    while (cluster < kAttnMaxCluster && pairs * cluster * 2 <= slots) cluster *= 2;
+    const int keys = D == 256 && pairs > slots ? kDirectKeysQueued : kDirectKeys;
+    if (max_len <= (long long)keys * cluster && pairs < (1 << 24)) return AttnPlan{0, cluster};
+    const long long most = pairs * ((max_len + kAttnUnit - 1) / kAttnUnit);
+    return AttnPlan{(int)std::min(std::max(most, 2LL), (long long)kAttnSms * kAttnCtasPerSm(D)), 0};
 }
 
 template <int D, bool F16>

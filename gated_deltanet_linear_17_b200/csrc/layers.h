@@ -49,12 +49,17 @@ struct RopeParams {
 };
 cudaError_t launch_rope(const RopeParams &p, int act_dtype, bool interleaved, cudaStream_t st);
 
-// The paged attention's grid: CTAs that fill a B200 (148 SMs) once, or one for each unit of kAttnUnit
-// keys where max_len (the longest sequence that the caller expects) leaves fewer; any count is right.
-constexpr int kAttnUnit = 64, kAttnSms = 148;
+constexpr int kAttnUnit = 64, kAttnSms = 148, kAttnMaxCluster = 8;
 constexpr int kAttnCtasPerSm(int D) { return D == 64 ? 3 : 2; }
+constexpr int kDirectCtasPerSm(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
 constexpr int kAttnMaxCtas = kAttnSms * 3;
-int attn_ctas(int B, int Hq, int Hkv, int D, long long max_len);
+// The paged attention's grid, by the sizes and the longest sequence that the caller expects; any is right for any
+// lengths.  direct: CTAs of the cluster that takes a pair of a sequence and a head group, or 0; then ctas fill
+// the GPU once (fewer where there is one for each kAttnUnit keys) and share all pairs evenly.
+struct AttnPlan {
+    int ctas, direct;
+};
+AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len);
 
 struct AttnParams {
     const void *q, *k, *v;
@@ -66,7 +71,7 @@ struct AttnParams {
     float2 *part_ml;  // [ctas][2][16]: a piece's maximum (base 2) and sum of exponentials
     float *part;      // [ctas][2][16][D]: its unnormalised sum
     float scale_log2;
-    int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages, ctas;
+    int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages, ctas, direct;
     FastDiv by_page;
 };
 cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, cudaStream_t st);

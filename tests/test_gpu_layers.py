@@ -476,6 +476,18 @@ def test_attn_scores_of_every_size():
     check_attn(q, c, scale=2.0)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_scores_far_below_zero(D):
+    """Scores of some -1000 for every key: what stands for the maximum of a part without keys must not be above them."""
+    lens = [1, 70, 0, 300, 129, 64, 513, 2000, 5]
+    c = Paged(lens, 1, D, 16, BF16, seed=21)
+    q = 1 + 0.1 * randn(gen(21), len(lens), 3, D)
+    for t in [c.k] + c.keys:
+        t.copy_(-t.abs() - 2)
+    for hint in (0, 2000, 64, 1 << 20):
+        check_attn(q, c, scale=500.0 / D, max_seqlen=hint)
+
+
 def test_attn_infinite_scores():
     """Keys whose score is -infinity weigh nothing; a row of nothing else is a zero row, as a row without keys."""
     c = Paged([40, 40], 1, 64, 16, BF16, seed=7)
@@ -646,13 +658,13 @@ def test_layers_captured_and_replayed():
     B, width, Hq, Hkv, page = 2, 128, 4, 1, 16
     proj = [randn(g, width, n * 128) * 0.06 for n in (Hq, Hkv, Hkv)] + [randn(g, Hq * 128, width) * 0.04]
     w = randn(g, width)
-    c = [Paged([1999, 700], Hkv, 128, page, BF16, seed=s, columns=126) for s in (1, 2)]
+    c = [Paged([3999, 700], Hkv, 128, page, BF16, seed=s, columns=251) for s in (1, 2)]
     f, _ = gdn.rope_inv_freq(64)
-    nbytes = gdn.paged_attn_workspace_bytes(B, Hq, Hkv, 128, page, 126, 2000)
+    nbytes = gdn.paged_attn_workspace_bytes(B, Hq, Hkv, 128, page, 251, 4000)
     assert nbytes > 0
     graphs, outs, args = [], [], []
     for cc in c:
-        lens = torch.tensor([2000, 701], dtype=torch.int32, device="cuda")
+        lens = torch.tensor([4000, 701], dtype=torch.int32, device="cuda")
         pos = lens - 1
         last = (pos // page).long()
         # a fresh page where the sequence's new token starts one
@@ -662,7 +674,7 @@ def test_layers_captured_and_replayed():
         slots = (cc.table[torch.arange(B, device="cuda"), last] * page + pos % page).to(torch.int32)
         x, r = randn(g, B, width), randn(g, B, width)
         ws = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-        a = (x, r, w, (cc.k, cc.v), cc.table, pos, lens, slots, f, proj, 2000, ws)
+        a = (x, r, w, (cc.k, cc.v), cc.table, pos, lens, slots, f, proj, 4000, ws)
         args.append(a)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -719,6 +731,7 @@ def test_attn_allocates_its_own_workspace_in_the_library():
     """A C call without a workspace: allocated and freed on the stream."""
     from gated_deltanet_linear_17_b200 import _layers
     c = Paged([5000, 20], 2, 128, 16, BF16, seed=9)
+    assert gdn.paged_attn_workspace_bytes(2, 8, 2, 128, 16, c.max_pages) > 0
     q = randn(gen(17), 2, 8, 128)
     want, _ = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens)
     out = torch.empty_like(q)
