@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     constexpr int kGroupLanes = kEl ? 32 : 128 / N;  // lanes that hold a group of 128 columns
     __shared__ float red[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
+    begin_early();
     const int t = L <= 32 ? (int)threadIdx.x % L : (int)threadIdx.x;
     const int width = KIND == kFull ? PER * L : p.width, quant = p.quant;
     const int v0 = kEl ? (t >> 5) * 128 + (t & 31) : t * N;  // place of this thread's first element, phase added
@@ -463,8 +464,7 @@ cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
     }
     const int per_sm = std::max(1, std::min(norm_ctas(L), (int)(kNormSmem / (smem + 1280))));
     const long long want = (p.rows + rows - 1) / rows;
-    kern<<<(unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_early(kern, (unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem, st, p);
 }
 
 // The threads of a row: the fewest of those built that hold `places` places, at least `least`.

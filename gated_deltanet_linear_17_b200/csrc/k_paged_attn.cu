@@ -13,7 +13,7 @@
 // has to be known on the host.  A part covers the end of one (sequence, head) pair, whole pairs, and
 // the beginning of another.  Whole pairs are written out; an incomplete one leaves its unnormalised sum,
 // maximum and sum of exponentials in one of the CTA's two places in the workspace, and a second kernel
-// (started early by a programmatic dependency) joins a pair's pieces in their order, so the result does
+// joins a pair's pieces in their order, so the result does
 // not depend on the order in which CTAs run.
 //
 // Short sequences (attn_direct) do without the list, the workspace and the second kernel: each pair is one
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
     __shared__ float2 joined[kRows];  // DIRECT: maximum and sum of this CTA's part of the keys
-    if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;");
+    begin_early();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const uint32_t qs = smem_addr(smem) + kWarps * S::kRing;
@@ -530,42 +530,56 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 // Joins the pieces of every pair that a CTA of the first kernel began and did not finish: piece 0 lies in
 // that CTA's place 1, piece j in place 0 of the j-th CTA after it.  Every CTA reads the list of such pairs;
 // a query head of a pair of few pieces is one warp's work, of many pieces (a long sequence cut over the whole
-// GPU) one CTA's for each 128 columns, its threads spread over the pieces.
-constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32, kJoinCtas = kAttnSms, kFewPieces = 4;
+// GPU) one CTA's for each 32 columns, its threads spread over the pieces.  Its CTAs are small enough (8K registers,
+// 13 KB) to lie beside the first kernel's on every SM before that ends; what is left behind its end is then two
+// loads, one waiting for the other.
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtas = kAttnSms, kFewPieces = 4;
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const AttnParams p)
 {
-    constexpr int kBlock = D < 128 ? D : 128, kBlocks = D / kBlock;   // columns of a CTA's item, items of a row
+    constexpr int kBlock = 32, kBlocks = D / kBlock;                  // columns of a CTA's item, items of a row
     constexpr int kCols = kBlock / 4, kGroups = kJoinThreads / kCols;  // threads along the columns, along the pieces
-    constexpr int kPer = (kAttnMaxCtas + kJoinThreads - 1) / kJoinThreads;
-    static_assert(kPer == 1, "a thread takes one CTA's record");
+    constexpr int kPer = (kAttnMaxCtas + kJoinThreads - 1) / kJoinThreads;  // records a thread takes
     __shared__ int4 list[kAttnMaxCtas];
     __shared__ uint32_t upto[kAttnMaxCtas], warp_total[kJoinWarps];  // many << 16 | few: items up to and with this one
-    __shared__ float weight[kAttnMaxCtas], red[2][kJoinWarps];
     __shared__ float4 part[kGroups][kCols];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float2 part_ml[kGroups];
+    constexpr int kInFlight = 5;  // pieces that a thread reads at a time: 296 CTAs cut two pairs into 148 pieces, 9.25 a thread
+    begin_early();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    uint32_t sum_items = 0;
-    if (tid < p.ctas) {
-        const int4 r = p.begun[tid];
-        list[tid] = r;
-        if (r.w > 0) sum_items = r.w > kFewPieces ? (uint32_t)(r.z * kBlocks) << 16 : (uint32_t)r.z;
+    uint32_t items[kPer], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int at = tid * kPer + i;
+        items[i] = 0;
+        if (at < p.ctas) {
+            const int4 r = p.begun[at];
+            list[at] = r;
+            if (r.w > 0) items[i] = r.w > kFewPieces ? (uint32_t)(r.z * kBlocks) << 16 : (uint32_t)r.z;
+        }
+        mine += items[i];
     }
+    uint32_t run = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, sum_items, d);
-        if (lane >= d) sum_items += y;
+        const uint32_t y = __shfl_up_sync(0xffffffffu, run, d);
+        if (lane >= d) run += y;
     }
-    if (lane == 31) warp_total[warp] = sum_items;
+    if (lane == 31) warp_total[warp] = run;
     __syncthreads();
     uint32_t total = 0;
+    run -= mine;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) {
-        if (w < warp) sum_items += warp_total[w];
+        if (w < warp) run += warp_total[w];
         total += warp_total[w];
     }
-    if (tid < p.ctas) upto[tid] = sum_items;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        run += items[i];
+        if (tid * kPer + i < p.ctas) upto[tid * kPer + i] = run;
+    }
     __syncthreads();
     const int many = total >> 16, few = total & 0xffff;
     // record that holds item `item` of a kind, and the item's number in it
@@ -617,43 +631,52 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const Att
         const int first = find(item, 16, &inner), row = inner / kBlocks, block = inner % kBlocks;
         const int4 rec = list[first];
         const int count = rec.w;
-        float top = -INFINITY;
-        for (int j = tid; j < count; j += kJoinThreads) top = fmaxf(top, p.part_ml[place(first, j, row)].x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        if (lane == 0) red[0][warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[0][w]);
-        top = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        for (int j = tid; j < count; j += kJoinThreads) {
-            const float2 ml = p.part_ml[place(first, j, row)];
-            const float w = exp2f(ml.x - top);
-            weight[j] = w;
-            sum += w * ml.y;
-        }
-        sum = warp_sum(sum);
-        if (lane == 0) red[1][warp] = sum;
-        __syncthreads();
-        sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) sum += red[1][w];
         const int c = block * kCols + tid % kCols, g = tid / kCols;
+        // this thread's pieces g, g + kGroups, ..: maxima, sums and columns in one go, joined as they come
+        float top = -INFINITY, sum = 0.f;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int j = g; j < count; j += kGroups) {
-            const float4 y = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[c];
-            const float w = weight[j];
-            x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
+        for (int j0 = g; j0 < count; j0 += kGroups * kInFlight) {
+            float2 ml[kInFlight];
+            float4 y[kInFlight];
+            float now = top;
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                const int j = j0 + i * kGroups;
+                ml[i] = make_float2(-INFINITY, 0.f);
+                y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < count) {
+                    ml[i] = p.part_ml[place(first, j, row)];
+                    y[i] = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[c];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) now = fmaxf(now, ml[i].x);
+            const float ref = now == -INFINITY ? 0.f : now, keep = exp2f(top - ref);
+            x.x *= keep, x.y *= keep, x.z *= keep, x.w *= keep, sum *= keep;
+#pragma unroll
+            for (int i = 0; i < kInFlight; ++i) {
+                const float w = exp2f(ml[i].x - ref);
+                sum = fmaf(w, ml[i].y, sum);
+                x.x = fmaf(w, y[i].x, x.x), x.y = fmaf(w, y[i].y, x.y);
+                x.z = fmaf(w, y[i].z, x.z), x.w = fmaf(w, y[i].w, x.w);
+            }
+            top = now;
         }
         part[g][tid % kCols] = x;
+        if (tid % kCols == 0) part_ml[g] = make_float2(top, sum);
         __syncthreads();
         if (g == 0) {
+            top = -INFINITY;
 #pragma unroll
-            for (int i = 1; i < kGroups; ++i) {
+            for (int i = 0; i < kGroups; ++i) top = fmaxf(top, part_ml[i].x);
+            top = top == -INFINITY ? 0.f : top;
+            x = make_float4(0.f, 0.f, 0.f, 0.f), sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
                 const float4 y = part[i][tid];
-                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                const float w = exp2f(part_ml[i].x - top);
+                sum = fmaf(w, part_ml[i].y, sum);
+                x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
             }
             write(rec, row, c, x, top, sum);
         }
@@ -674,30 +697,23 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
         cfg.blockDim = dim3(S::kThreads);
         cfg.dynamicSmemBytes = S::kSmem;
         cfg.stream = st;
-        cudaLaunchAttribute at[1];
+        cudaLaunchAttribute at[2];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = (unsigned)p.direct;
         at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = at;
-        cfg.numAttrs = 1;
+        cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, kern, p);
     }
     using S = Shape<D, NT, false>;
     const auto kern = paged_attn_kernel<D, NT, F16, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)p.ctas, S::kThreads, S::kSmem, st>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kJoinCtas);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_attn_join_kernel<D, F16>, p);
+    e = launch_early(kern, (unsigned)p.ctas, S::kThreads, S::kSmem, st, p);
+    if (e != cudaSuccess) return e;
+    return launch_early(paged_attn_join_kernel<D, F16>, kJoinCtas, kJoinThreads, 0, st, p);
 }
 
 }  // namespace

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(typename A::raw
 {
     using raw = typename A::raw;
     extern __shared__ __align__(16) float2 angles[];  // [tokens of the CTA][n, rounded up to an even number]
+    begin_early();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int D = DIM ? DIM : p.D, n = p.n, pitch = (n + 1) & ~1;
     const int lanes = D / 8, per = 32 / lanes;  // lanes a row, tokens a warp
@@ -181,12 +182,11 @@ cudaError_t launch_dim(const RopeParams &p, cudaStream_t st)
     const unsigned grid = (unsigned)((p.T + tokens - 1) / tokens);
     const size_t smem = sizeof(float2) * tokens * ((p.n + 1) & ~1);
     switch (p.D) {
-    case 64: rope_kernel<A, LAYOUT, 64><<<grid, kRopeThreads, smem, st>>>(p); break;
-    case 128: rope_kernel<A, LAYOUT, 128><<<grid, kRopeThreads, smem, st>>>(p); break;
-    case 256: rope_kernel<A, LAYOUT, 256><<<grid, kRopeThreads, smem, st>>>(p); break;
-    default: rope_kernel<A, LAYOUT, 0><<<grid, kRopeThreads, smem, st>>>(p); break;
+    case 64: return launch_early(rope_kernel<A, LAYOUT, 64>, grid, kRopeThreads, smem, st, p);
+    case 128: return launch_early(rope_kernel<A, LAYOUT, 128>, grid, kRopeThreads, smem, st, p);
+    case 256: return launch_early(rope_kernel<A, LAYOUT, 256>, grid, kRopeThreads, smem, st, p);
+    default: return launch_early(rope_kernel<A, LAYOUT, 0>, grid, kRopeThreads, smem, st, p);
     }
-    return cudaGetLastError();
 }
 
 template <class A>

@@ -7,6 +7,32 @@
 
 namespace gdn {
 
+// ---------------------------------------------------------------- launches that overlap their predecessor's end
+// Every kernel of gdn_layers.h is launched with launch_early: its CTAs may come to lie on the SMs while the
+// kernel before it in the stream is still at work, and wait in begin_early, before their first access to memory,
+// until that one is complete and its writes visible.  A kernel that has called begin_early lets its own successor
+// in likewise (once all its CTAs run, so the successor takes no room from them).
+__device__ __forceinline__ void begin_early()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <class K, class P>
+cudaError_t launch_early(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t st, const P &p)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 // ---------------------------------------------------------------- 8 elements at a time
 // (16 bytes of a 16-bit type, 32 of fp32; the address is 16-byte aligned)
 struct Bf16 {
