@@ -101,7 +101,10 @@ __device__ __forceinline__ bool bad_length(int n, const AttnParams &p)
 // that stand for what a pair costs beside its keys (its queries, the first page's latency, its output), so
 // that a CTA of many short pairs gets no more work than one of a long pair.
 template <int D>
-constexpr int kLead = D == 64 ? 3 : D == 128 ? 2 : 1;
+#ifndef L64
+#define L64 3
+#endif
+constexpr int kLead = D == 64 ? L64 : D == 128 ? 2 : 1;
 template <int D>
 __device__ __forceinline__ int places(int n, const AttnParams &p)
 {
@@ -604,25 +607,31 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
         const int4 rec = list[first];
         float2 ml = make_float2(-INFINITY, 0.f);
         if (lane < rec.w) ml = p.part_ml[place(first, lane, row)];
+        constexpr int kPerLane = (D / 4 + 31) / 32;  // columns (by fours) lane, lane + 32
+        float4 y[kPerLane][kFewPieces];
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+#pragma unroll
+            for (int j = 0; j < kFewPieces; ++j) {
+                y[i][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (j < rec.w && lane + 32 * i < D / 4)
+                    y[i][j] = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[lane + 32 * i];
+            }
         float top = ml.x;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         top = top == -INFINITY ? 0.f : top;
         const float w = exp2f(ml.x - top), sum = warp_sum(w * ml.y);
-        float wj[kFewPieces];
 #pragma unroll
-        for (int j = 0; j < kFewPieces; ++j) wj[j] = __shfl_sync(0xffffffffu, w, j);
-#pragma unroll
-        for (int c = lane; c < D / 4; c += 32) {
+        for (int i = 0; i < kPerLane; ++i) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int j = 0; j < kFewPieces; ++j) {
-                if (j >= rec.w) break;
-                const float4 y = reinterpret_cast<const float4 *>(p.part + place(first, j, row) * D)[c];
-                x.x = fmaf(wj[j], y.x, x.x), x.y = fmaf(wj[j], y.y, x.y);
-                x.z = fmaf(wj[j], y.z, x.z), x.w = fmaf(wj[j], y.w, x.w);
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+                x.x = fmaf(wj, y[i][j].x, x.x), x.y = fmaf(wj, y[i][j].y, x.y);
+                x.z = fmaf(wj, y[i][j].z, x.z), x.w = fmaf(wj, y[i][j].w, x.w);
             }
-            write(rec, row, c, x, top, sum);
+            if (lane + 32 * i < D / 4) write(rec, row, lane + 32 * i, x, top, sum);
         }
     }
 
