@@ -111,13 +111,25 @@ __device__ __forceinline__ int places(int n, const AttnParams &p)
     return kLead<D> + (bad_length(n, p) ? 0 : (n + kAttnUnit - 1) / kAttnUnit);
 }
 
+// i total / n rounded down, and the part of n equal ones that holds place u: the largest i with i total / n <= u.
+// 64-bit divisions take a microsecond of a CTA's start between them; lists of up to 2^22 places do without.
+__device__ __forceinline__ long long part_begin(long long total, int i, int n)
+{
+    return total < (1 << 22) ? (long long)((uint32_t)total * (uint32_t)i / (uint32_t)n) : total * i / n;
+}
+__device__ __forceinline__ int part_of(long long total, long long u, int n)
+{
+    return total < (1 << 22) ? (int)((((uint32_t)u + 1) * (uint32_t)n - 1) / (uint32_t)total)
+                             : (int)(((u + 1) * n - 1) / total);
+}
+
 // where a CTA's part of the list begins, and the list's length
 struct Part {
-    long long first, total;
+    long long first, last, total;  // the part's first place, and the one behind it
     int ctas;        // CTAs that have a part: the grid, or fewer where there are fewer places (so that no part in
                      // between is empty and a pair's pieces lie in neighbouring CTAs)
-    int b;           // sequence of the first place
-    long long rest;  // places before it in its sequence, over all heads
+    int b, n;        // sequence of the first place, and its length
+    int pair, u0;    // head group of the first place, and its number there
 };
 
 // All threads call it.  Thread t sums the places of its run of sequences; a scan over the threads finds the
@@ -132,7 +144,11 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     const int run = (p.B + kThreads - 1) / kThreads, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
     const int heads = p.Hkv * p.row_tiles;
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += places<D>(p.lens[b], p);
+    int n = 0;
+    for (int b = b1 - 1; b >= b0; --b) {
+        n = p.lens[b];
+        mine += places<D>(n, p);
+    }
     long long upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -148,16 +164,21 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
         total += warp_total[w];
     }
     total *= heads;
-    const int ctas = (int)min(total, (long long)gridDim.x);
-    const long long first = total * blockIdx.x / ctas;  // past the list for a CTA without a part
+    const int ctas = (int)min(total, (long long)gridDim.x), i = blockIdx.x;
+    const long long first = part_begin(total, i, ctas);  // past the list for a CTA without a part
     const long long begin = (upto - mine) * heads;
     if (first >= begin && first < upto * heads) {
-        long long rest = first - begin;
-        int b = b0;
-        for (long long n; rest >= (n = (long long)places<D>(p.lens[b], p) * heads); ++b) rest -= n;
-        found = Part{first, total, ctas, b, rest};
+        long long rest = first - begin;  // places before the first in the run, then in its sequence
+        int b = b0, each;
+        for (;; n = p.lens[++b]) {  // n: the length of sequence b
+            each = places<D>(n, p);
+            if (rest < (long long)each * heads) break;
+            rest -= (long long)each * heads;
+        }
+        const int pair = rest < (1LL << 31) ? (int)((uint32_t)rest / (uint32_t)each) : (int)(rest / each);
+        found = Part{first, part_begin(total, i + 1, ctas), total, ctas, b, n, pair, (int)(rest - (long long)pair * each)};
     }
-    if (tid == 0 && (int)blockIdx.x >= ctas) found.ctas = ctas;
+    if (tid == 0 && i >= ctas) found.ctas = ctas;
     __syncthreads();
     return found;
 }
@@ -231,13 +252,13 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             if (tid == 0) p.begun[blockIdx.x] = begun;
             return;
         }
-        left_places = part.total * (blockIdx.x + 1) / part.ctas - part.first;
+        left_places = part.last - part.first;
         pos = part.first;
         b = part.b;
-        n_raw = p.lens[b];
+        n_raw = part.n;
         u_all = places<D>(n_raw, p);
-        pair = (int)(part.rest / u_all);
-        u0 = (int)(part.rest - (long long)pair * u_all);
+        pair = part.pair;
+        u0 = part.u0;
     }
 
     for (;;) {
@@ -510,9 +531,8 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         return;
     }
     if (!whole && u0 == 0) {
-        // the CTA that holds the pair's last place u: the largest i with floor(i total / ctas) <= u
-        const long long last = pos + u_all - 1;
-        const int until = (int)(((last + 1) * part.ctas - 1) / part.total);
+        // the CTA that holds the pair's last place
+        const int until = part_of(part.total, pos + u_all - 1, part.ctas);
         begun = make_int4(b, head0, rows, until - (int)blockIdx.x + 1);
     }
     left_places -= take;
