@@ -49,41 +49,38 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _need(t, name, dtype, shape, dev):
-    """``_binding._need``, with the comparisons of a good tensor kept cheap (a decode step's calls are short)."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev
+def _need(t, name, dtype, shape, index):
+    """``_binding._need`` (on CUDA device ``index``), with the comparisons of a good tensor kept cheap: a decode step's
+    calls take a few microseconds."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
-        _b._need(t, name, dtype, shape, dev)
+        _b._need(t, name, dtype, shape, torch.device("cuda", index))
 
 
 @contextlib.contextmanager
-def _on(dev, stream):
-    """``dev`` and ``stream`` (or the device's current stream) as the current ones."""
-    if stream is not None and stream.device != dev:
-        raise RuntimeError(f"the stream is on {stream.device}, the tensors on {dev}")
-    with torch.cuda.device(dev), torch.cuda.stream(stream):
+def _on(index, stream):
+    """Device ``index`` and ``stream`` (or the device's current stream) as the current ones."""
+    if stream is not None and stream.device.index != index:
+        raise RuntimeError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
         yield
 
 
-def _elsewhere(dev, stream):
-    """Whether a call on ``dev`` and ``stream`` has to change the current device or stream first."""
-    return stream is not None or dev.index != torch.cuda.current_device()
-
-
-def _stream_of(dev):
-    # the handle alone: a tenth of a microsecond against more than one for a Stream object
-    return torch._C._cuda_getCurrentRawStream(dev.index)
+# the current device, and the current stream's handle on a device: each a tenth of what torch.cuda's own take
+_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
 def _cuda(t, name):
+    """The index of the CUDA device that t lies on."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0 or not t.is_cuda:
         raise RuntimeError(f"{name} must be on a CUDA device (got {t.device})")
+    return index
 
 
 def _act(t, name, types=_b.DTYPES):
-    _cuda(t, name)
     if t.dtype not in types:
         raise RuntimeError(f"{name} must be one of {[str(d) for d in types]} (got {t.dtype})")
     return t.dtype
@@ -101,17 +98,18 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
     row, [...]; "block" one per row and 128 columns, [..., ceil(width / 128)]: y is about out * scale.
     ``out`` may be x (without ``quant``) and ``residual_out`` may be the residual: then they are
     updated in place."""
-    act = _act(x, "x")
-    if _elsewhere(x.device, stream):
-        with _on(x.device, stream):
+    dev = _cuda(x, "x")
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
             return rms_norm(x, weight, residual, gate, eps, weight_offset, quant, out, residual_out, scales)
     if quant not in QUANT:
         raise ValueError(f"quant must be one of {list(QUANT)} (got {quant!r})")
     if x.dim() < 1 or x.shape[-1] < 1:
         raise ValueError("x must be [..., width] with at least one column")
-    shape, dev = x.shape, x.device
+    act, shape = _act(x, "x"), x.shape
     width = shape[-1]
-    _need(x, "x", act, shape, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     _cuda(weight, "weight")
     wdt = torch.float32 if weight.dtype == torch.float32 else act
     _need(weight, "weight", wdt, (width,), dev)
@@ -140,7 +138,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
         scales = x.new_empty(sshape, dtype=torch.float32)
     rc = _layers_lib().gdn_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), eps, weight_offset, _ptr(out),
                                     _ptr(residual_out), _ptr(scales), x.numel() // width, width, _b.DTYPES[act],
-                                    _b.DTYPES[wdt], QUANT[quant], _stream_of(dev))
+                                    _b.DTYPES[wdt], QUANT[quant], _current_stream(dev))
     _b._check(rc, "gdn_rms_norm")
     return out, residual_out, scales
 
@@ -192,18 +190,18 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     also go to the cache rows ``slots`` [T] int32 (page * page_size + place in the page; a slot
     outside the cache marks a padding token, which is not written; slots have to differ), and the turned
     keys are returned only if ``k_out`` is given (else None).  ``q_out`` may be q, ``k_out`` may be k."""
-    act = _act(q, "q")
-    if _elsewhere(q.device, stream):
-        with _on(q.device, stream):
+    dev = _cuda(q, "q")
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
             return rope_fwd(q, k, positions, inv_freq, v, k_cache, v_cache, slots, interleaved, mscale, q_out, k_out)
-    if q.dim() != 3:
-        raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     _cuda(k, "k")
-    if k.dim() != 3:
+    if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
+    act = _act(q, "q")
     T, Hq, D = q.shape
-    Hkv, dev = k.shape[1], q.device
-    _need(q, "q", act, (T, Hq, D), dev)
+    Hkv = k.shape[1]
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     _need(k, "k", act, (T, Hkv, D), dev)
     _need(positions, "positions", torch.int32, (T,), dev)
     _cuda(inv_freq, "inv_freq")
@@ -235,7 +233,7 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     rc = _layers_lib().gdn_rope_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(slots), mscale,
                                     _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D,
                                     2 * inv_freq.shape[0], 1 if interleaved else 0, rows, _b.DTYPES[act],
-                                    _stream_of(dev))
+                                    _current_stream(dev))
     _b._check(rc, "gdn_rope_fwd")
     return q_out, k_out
 
@@ -260,18 +258,18 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     ``lse`` [B, Hq] fp32 is written when given or when ``output_lse``.  ``workspace``: a device buffer
     of ``paged_attn_workspace_bytes`` bytes, allocated here when not given; calls that can overlap on
     the GPU, replayed graphs among them, need buffers of their own."""
-    act = _act(q, "q", (torch.bfloat16, torch.float16))
-    if _elsewhere(q.device, stream):
-        with _on(q.device, stream):
+    dev = _cuda(q, "q")
+    if stream is not None or dev != _current_device():
+        with _on(dev, stream):
             return paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, max_seqlen, out, lse, output_lse,
                                   workspace)
+    act = _act(q, "q", (torch.bfloat16, torch.float16))
     _cuda(k_cache, "k_cache")
     _cuda(block_table, "block_table")
     if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
         raise ValueError("q must be [B, Hq, D], the caches [P, page_size, Hkv, D] and block_table [B, max_pages]")
     B, Hq, D = q.shape
-    P, page, Hkv = k_cache.shape[:3]
-    dev = q.device
+    P, page, Hkv, _ = k_cache.shape
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"Hq ({Hq}) must be a multiple of Hkv ({Hkv})")
     if page < 1:
@@ -280,7 +278,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
     max_pages = block_table.shape[1]
-    _need(q, "q", act, (B, Hq, D), dev)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
     _need(k_cache, "k_cache", act, (P, page, Hkv, D), dev)
     _need(v_cache, "v_cache", act, (P, page, Hkv, D), dev)
     _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
@@ -290,9 +289,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq), dev)
     if workspace is not None:
-        _cuda(workspace, "workspace")
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise RuntimeError(f"workspace must be a contiguous tensor on {dev}")
+        if _cuda(workspace, "workspace") != dev or not workspace.is_contiguous():
+            raise RuntimeError(f"workspace must be a contiguous tensor on cuda:{dev}")
     if out is None:
         out = torch.empty_like(q)
     if lse is None and output_lse:
@@ -305,6 +303,6 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     rc = _layers_lib().gdn_paged_attn_fwd(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
                                           0.0 if scale is None else scale, _ptr(out), _ptr(lse), B, Hq, Hkv, D, P,
                                           page, max_pages, max_seqlen, _b.DTYPES[act], _ptr(workspace), ws_bytes,
-                                          _stream_of(dev))
+                                          _current_stream(dev))
     _b._check(rc, "gdn_paged_attn_fwd")
     return out, lse
