@@ -274,7 +274,7 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
         raise ValueError(f"Hq ({Hq}) must be a multiple of Hkv ({Hkv})")
     if page < 1:
         raise ValueError("page_size must be at least 1")
-    max_seqlen = int(max_seqlen)
+    max_seqlen = min(int(max_seqlen), 0x7fffffff)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
     max_pages = block_table.shape[1]

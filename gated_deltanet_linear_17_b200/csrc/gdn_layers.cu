@@ -5,6 +5,7 @@
 
 #include <algorithm>
 
+#include "gdn_testing.h"
 #include "layers.h"
 
 namespace {
@@ -177,17 +178,64 @@ int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, 
         workspace = own;
     }
     gdn::AttnParams p;
-    p.q = q, p.k = k_cache, p.v = v_cache, p.table = block_table, p.lens = seq_lens, p.out = out, p.lse = lse;
+    // (without a page nothing is read of the caches, but the copies of absent keys name a mapped address)
+    p.q = q, p.k = P > 0 ? k_cache : q, p.v = P > 0 ? v_cache : q, p.table = block_table, p.lens = seq_lens, p.out = out, p.lse = lse;
     p.begun = static_cast<int4 *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.begun + plan.ctas);
     p.part = reinterpret_cast<float *>(p.part_ml + 32 * (size_t)plan.ctas);
     p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.44269504f;
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.group = Hq / Hkv, p.row_tiles = (Hq / Hkv + 15) / 16;
     p.P = P, p.page_size = page_size, p.max_pages = max_pages, p.ctas = plan.ctas, p.direct = plan.direct;
+    p.capacity = (long long)page_size * max_pages;
     p.by_page = gdn::FastDiv((uint32_t)page_size);
     rc = cuda_status(gdn::launch_paged_attn(p, D, act_dtype == GDN_DTYPE_FP16, st));
     if (own && cudaFreeAsync(own, st) != cudaSuccess && rc == GDN_OK) rc = GDN_ERR_CUDA;
     return rc;
+}
+
+int gdn_testing_attn_split(const int32_t *lens, int32_t B, int32_t heads, int32_t D, int64_t capacity, int32_t ctas,
+                           int32_t *pieces, int32_t max_pieces)
+{
+    if (!lens || !pieces || B <= 0 || heads <= 0 || ctas <= 0 || capacity < 0 || (D != 64 && D != 128 && D != 256))
+        return -1;
+    int64_t total = 0;
+    for (int b = 0; b < B; ++b) total += (int64_t)gdn::attn_places(D, lens[b], capacity) * heads;
+    const int parts = (int)std::min<int64_t>(total, ctas);
+    int count = 0, b = 0, group = 0, u0 = 0;
+    for (int i = 0; i < parts; ++i) {
+        int64_t at = gdn::attn_part_begin(total, i, parts);
+        const int64_t end = gdn::attn_part_begin(total, i + 1, parts);
+        while (at < end) {
+            const int all = gdn::attn_places(D, lens[b], capacity), n = gdn::attn_refused(lens[b], capacity) ? 0 : lens[b];
+            const int take = (int)std::min<int64_t>(all - u0, end - at);
+            if (count >= max_pieces) return -1;
+            const gdn::KeyRange k = gdn::attn_keys(D, u0, take, n);
+            int32_t *r = pieces + 7 * (int64_t)count++;
+            r[0] = i, r[1] = b, r[2] = group, r[3] = k.k0, r[4] = k.k1;
+            r[5] = take == all ? 2 : u0 == 0;
+            r[6] = take < all && u0 == 0 ? gdn::attn_part_of(total, at + all - 1, parts) - i + 1 : 0;
+            at += take, u0 += take;
+            if (u0 == all) {
+                u0 = 0;
+                if (++group == heads) group = 0, ++b;
+            }
+        }
+    }
+    return count;
+}
+
+int gdn_testing_attn_cluster(int32_t n, int32_t cluster, int32_t rank, int32_t *k0, int32_t *k1)
+{
+    if (n < 0 || cluster <= 0 || rank < 0 || rank >= cluster || !k0 || !k1) return -1;
+    const gdn::KeyRange k = gdn::attn_cluster_keys(rank, cluster, n);
+    *k0 = k.k0, *k1 = k.k1;
+    return 0;
+}
+
+int gdn_testing_attn_row(const int32_t *pages, int32_t j, int32_t page_size, int32_t P)
+{
+    if (!pages || j < 0 || page_size <= 0 || P < 0) return -2;
+    return gdn::attn_cache_row(pages, j, gdn::FastDiv((uint32_t)page_size), page_size, P);
 }
 
 }  // extern "C"

@@ -92,37 +92,6 @@ __device__ __forceinline__ float quad_sum(float x)
     return x + __shfl_xor_sync(0xffffffffu, x, 2);
 }
 
-// a length outside the table's range stands for the whole sequence being refused
-__device__ __forceinline__ bool bad_length(int n, const AttnParams &p)
-{
-    return n < 0 || n > (long long)p.max_pages * p.page_size;
-}
-// Places that one head of a sequence takes in the list: one for each kAttnUnit keys, behind kLead<D>
-// that stand for what a pair costs beside its keys (its queries, the first page's latency, its output), so
-// that a CTA of many short pairs gets no more work than one of a long pair.
-template <int D>
-#ifndef L64
-#define L64 3
-#endif
-constexpr int kLead = D == 64 ? L64 : D == 128 ? 2 : 1;
-template <int D>
-__device__ __forceinline__ int places(int n, const AttnParams &p)
-{
-    return kLead<D> + (bad_length(n, p) ? 0 : (n + kAttnUnit - 1) / kAttnUnit);
-}
-
-// i total / n rounded down, and the part of n equal ones that holds place u: the largest i with i total / n <= u.
-// 64-bit divisions take a microsecond of a CTA's start between them; lists of up to 2^22 places do without.
-__device__ __forceinline__ long long part_begin(long long total, int i, int n)
-{
-    return total < (1 << 22) ? (long long)((uint32_t)total * (uint32_t)i / (uint32_t)n) : total * i / n;
-}
-__device__ __forceinline__ int part_of(long long total, long long u, int n)
-{
-    return total < (1 << 22) ? (int)((((uint32_t)u + 1) * (uint32_t)n - 1) / (uint32_t)total)
-                             : (int)(((u + 1) * n - 1) / total);
-}
-
 // where a CTA's part of the list begins, and the list's length
 struct Part {
     long long first, last, total;  // the part's first place, and the one behind it
@@ -147,7 +116,7 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     int n = 0;
     for (int b = b1 - 1; b >= b0; --b) {
         n = p.lens[b];
-        mine += places<D>(n, p);
+        mine += attn_places(D, n, p.capacity);
     }
     long long upto = mine;
 #pragma unroll
@@ -165,18 +134,18 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     }
     total *= heads;
     const int ctas = (int)min(total, (long long)gridDim.x), i = blockIdx.x;
-    const long long first = part_begin(total, i, ctas);  // past the list for a CTA without a part
+    const long long first = attn_part_begin(total, i, ctas);  // past the list for a CTA without a part
     const long long begin = (upto - mine) * heads;
     if (first >= begin && first < upto * heads) {
         long long rest = first - begin;  // places before the first in the run, then in its sequence
         int b = b0, each;
         for (;; n = p.lens[++b]) {  // n: the length of sequence b
-            each = places<D>(n, p);
+            each = attn_places(D, n, p.capacity);
             if (rest < (long long)each * heads) break;
             rest -= (long long)each * heads;
         }
         const int pair = rest < (1LL << 31) ? (int)((uint32_t)rest / (uint32_t)each) : (int)(rest / each);
-        found = Part{first, part_begin(total, i + 1, ctas), total, ctas, b, n, pair, (int)(rest - (long long)pair * each)};
+        found = Part{first, attn_part_begin(total, i + 1, ctas), total, ctas, b, n, pair, (int)(rest - (long long)pair * each)};
     }
     if (tid == 0 && i >= ctas) found.ctas = ctas;
     __syncthreads();
@@ -256,7 +225,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         pos = part.first;
         b = part.b;
         n_raw = part.n;
-        u_all = places<D>(n_raw, p);
+        u_all = attn_places(D, n_raw, p.capacity);
         pair = part.pair;
         u0 = part.u0;
     }
@@ -265,20 +234,13 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     // this piece: keys [k0, k1) of head group `pair` of sequence b; of the list, places [u0, u0 + take)
     const int take = DIRECT ? 0 : (int)min(left_places, (long long)(u_all - u0));
     const bool whole = DIRECT ? p.direct == 1 : take == u_all;
-    const bool bad = bad_length(n_raw, p);
+    const bool bad = attn_refused(n_raw, p.capacity);
     const int n = bad ? 0 : n_raw;
     const int hkv = pair / p.row_tiles, tile_row0 = (pair - hkv * p.row_tiles) * kRows;
     const int rows = min(kRows, p.group - tile_row0);
     const int head0 = hkv * p.group + tile_row0;  // first query head of this piece
-    int k0, k1;
-    if (DIRECT) {
-        const int each = (n / p.direct + kTile) & ~(kTile - 1);  // above n / direct
-        k0 = min(n, rank * each);
-        k1 = min(n, k0 + each);
-    } else {
-        k0 = max(0, u0 - kLead<D>) * kAttnUnit;
-        k1 = min(n, max(0, u0 + take - kLead<D>) * kAttnUnit);
-    }
+    const KeyRange keys = DIRECT ? attn_cluster_keys(rank, p.direct, n) : attn_keys(D, u0, take, n);
+    const int k0 = keys.k0, k1 = keys.k1;
     const int n_next = !DIRECT && b + 1 < p.B ? p.lens[b + 1] : 0;
 
     // this warp's tiles: first + 16 (warp + 4 i)
@@ -290,12 +252,9 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     auto cache_row = [&](int i) {
         const int j = k0 + kTile * (warp + kWarps * i) + (lane & 15);
         if (i >= mine || j >= k1) return -1;
-        const int pg = (int)fast_div(j, p.by_page), page = table[pg];
-        if ((unsigned)page >= (unsigned)p.P) {
-            bad_page = true;
-            return -1;
-        }
-        return page * p.page_size + (j - pg * p.page_size);
+        const int row = attn_cache_row(table, j, p.by_page, p.page_size, p.P);
+        bad_page |= row < 0;
+        return row;
     };
     auto fetch = [&](int stage, int row) {
         const uint32_t dst = ring + stage * S::kStage;
@@ -532,7 +491,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     }
     if (!whole && u0 == 0) {
         // the CTA that holds the pair's last place
-        const int until = part_of(part.total, pos + u_all - 1, part.ctas);
+        const int until = attn_part_of(part.total, pos + u_all - 1, part.ctas);
         begun = make_int4(b, head0, rows, until - (int)blockIdx.x + 1);
     }
     left_places -= take;
@@ -543,7 +502,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         pair = 0;
         ++b;
         n_raw = n_next;
-        u_all = places<D>(n_raw, p);
+        u_all = attn_places(D, n_raw, p.capacity);
     }
     __syncthreads();  // the rings, the query rows and wm, wl are free again
     }

@@ -1,5 +1,5 @@
 // Device helpers shared by the kernels of gdn_layers.h: 8-element accesses of the three
-// activation types, and division by a run-time constant.
+// activation types, and launches that overlap.
 #pragma once
 
 #include "common.cuh"
@@ -124,10 +124,5 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     return (uint32_t)hi << 16 | lo;
 }
 __device__ __forceinline__ uint8_t to_e4m3(float a) { return (uint8_t)(pack_e4m3(a, 0.f, 0.f, 0.f) & 0xff); }
-
-__device__ __forceinline__ uint32_t fast_div(uint32_t n, FastDiv d)
-{
-    return d.shift < 0 ? n : (uint32_t)(((uint64_t)n * d.mul) >> 32 >> d.shift);
-}
 
 }  // namespace gdn

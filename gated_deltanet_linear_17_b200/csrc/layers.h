@@ -25,6 +25,11 @@ struct FastDiv {
     }
 };
 
+__host__ __device__ inline uint32_t fast_div(uint32_t n, FastDiv d)
+{
+    return d.shift < 0 ? n : (uint32_t)(((uint64_t)n * d.mul) >> 32 >> d.shift);
+}
+
 struct NormParams {
     const void *x, *residual, *gate, *weight;
     void *out, *residual_out;
@@ -61,6 +66,53 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len);
 
+// The list that the pairs of a sequence and a head group are cut by: one place for each kAttnUnit keys of a pair,
+// behind attn_lead places that stand for what a pair costs beside its keys (its queries, the first page's latency,
+// its output), so that a CTA of many short pairs gets no more work than one of a long pair.  Measured with 1, 3 and
+// 8 leading places at D = 64: 37 ragged sequences of 12 heads 58, 55, 57 us.
+__host__ __device__ constexpr int attn_lead(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
+// a length outside the table's capacity stands for the whole sequence being refused
+__host__ __device__ inline bool attn_refused(int n, long long capacity) { return n < 0 || n > capacity; }
+__host__ __device__ inline int attn_places(int D, int n, long long capacity)
+{
+    return attn_lead(D) + (attn_refused(n, capacity) ? 0 : (n + kAttnUnit - 1) / kAttnUnit);
+}
+// the keys of places [u0, u0 + take) of a pair of n keys
+struct KeyRange {
+    int k0, k1;
+};
+__host__ __device__ inline KeyRange attn_keys(int D, int u0, int take, int n)
+{
+    const int a = u0 - attn_lead(D), b = a + take;
+    const int k1 = b > 0 ? b * kAttnUnit : 0;
+    return KeyRange{a > 0 ? a * kAttnUnit : 0, k1 < n ? k1 : n};
+}
+// Part i of n equal ones of the list begins at i total / n, rounded down; place u lies in the last part that begins
+// at or before it.  64-bit divisions take a microsecond of a CTA's start between them; lists of up to 2^22 places
+// do without.
+__host__ __device__ inline long long attn_part_begin(long long total, int i, int n)
+{
+    return total < (1 << 22) ? (long long)((uint32_t)total * (uint32_t)i / (uint32_t)n) : total * i / n;
+}
+__host__ __device__ inline int attn_part_of(long long total, long long u, int n)
+{
+    return total < (1 << 22) ? (int)((((uint32_t)u + 1) * (uint32_t)n - 1) / (uint32_t)total)
+                             : (int)(((u + 1) * n - 1) / total);
+}
+// the keys that CTA `rank` of a cluster takes of n
+__host__ __device__ inline KeyRange attn_cluster_keys(int rank, int cluster, int n)
+{
+    const int each = (n / cluster + 16) & ~15;  // above n / cluster
+    const long long k0 = (long long)rank * each;
+    return KeyRange{(int)(k0 < n ? k0 : n), (int)(k0 + each < n ? k0 + each : n)};
+}
+// cache row of key j of a sequence whose pages `table` lists; -1 on a page outside the cache's P
+__host__ __device__ inline int attn_cache_row(const int32_t *table, int j, FastDiv by_page, int page_size, int P)
+{
+    const int nth = (int)fast_div((uint32_t)j, by_page), page = table[nth];
+    return (uint32_t)page < (uint32_t)P ? page * page_size + (j - nth * page_size) : -1;
+}
+
 struct AttnParams {
     const void *q, *k, *v;
     const int32_t *table, *lens;
@@ -72,6 +124,7 @@ struct AttnParams {
     float *part;      // [ctas][2][16][D]: its unnormalised sum
     float scale_log2;
     int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages, ctas, direct;
+    long long capacity;  // page_size * max_pages
     FastDiv by_page;
 };
 cudaError_t launch_paged_attn(const AttnParams &p, int D, bool f16, cudaStream_t st);

@@ -57,6 +57,27 @@ int gdn_selftest_wait(int32_t max_polls, int32_t arrive, void *workspace, size_t
 int gdn_testing_host_plan(const int32_t *cu_seqlens, int64_t T, int32_t B, int32_t segments, int32_t *calls,
                           int32_t max_calls);
 
+/*
+ * gdn_testing_attn_split: how gdn_paged_attn_fwd cuts its work over `ctas` CTAs
+ * where it does so by a list, on the host only, by the functions that the
+ * kernel uses.  For host int32 lens [B], `heads` head groups a sequence and a
+ * table of `capacity` keys a sequence it writes up to max_pieces rows of 7
+ * int32: CTA, sequence, head group, first key, end key, the place that the
+ * piece's result goes to (2: the piece is the whole pair and is written out;
+ * 1: the pair begins here; 0: it began in an earlier CTA), and the number of
+ * the pair's pieces (at its beginning; else 0).  Returns the number of pieces,
+ * or -1 for invalid arguments or too small a max_pieces.
+ */
+int gdn_testing_attn_split(const int32_t *lens, int32_t B, int32_t heads, int32_t D, int64_t capacity, int32_t ctas,
+                           int32_t *pieces, int32_t max_pieces);
+
+/* The keys [*k0, *k1) of n that CTA `rank` of a cluster takes (-1: invalid arguments, else 0). */
+int gdn_testing_attn_cluster(int32_t n, int32_t cluster, int32_t rank, int32_t *k0, int32_t *k1);
+
+/* The cache row of key j of a sequence with these host pages, or -1 where its page lies outside [0, P) (-2: invalid
+ * arguments): the bounds check of the kernel. */
+int gdn_testing_attn_row(const int32_t *pages, int32_t j, int32_t page_size, int32_t P);
+
 #ifdef __cplusplus
 }
 #endif

@@ -5,6 +5,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import random
 
 import pytest
 import torch
@@ -210,3 +211,101 @@ def test_inv_freq():
                 dict(rotary=64, factor=0.5), dict(rotary=64, beta_fast=1.0, beta_slow=2.0)):
         with pytest.raises(ValueError):
             gdn.rope_inv_freq(device="cpu", **bad)
+
+
+# ------------------------------------------------------------------ how the paged attention cuts its work
+
+
+def _split(lib, lens, heads, D, capacity, ctas):
+    cap = 4 * (len(lens) * heads + ctas)
+    rows = (ctypes.c_int32 * (7 * cap))()
+    n = lib.gdn_testing_attn_split((ctypes.c_int32 * len(lens))(*lens), len(lens), heads, D, ctypes.c_int64(capacity),
+                                   ctas, rows, cap)
+    assert n >= 0
+    return [tuple(rows[7 * i:7 * i + 7]) for i in range(n)]
+
+
+def _check_split(lib, lens, heads, D, capacity, ctas):
+    pieces = _split(lib, lens, heads, D, capacity, ctas)
+    keys, places, begun = {}, set(), {}
+    for cta, b, group, k0, k1, place, count in pieces:
+        assert 0 <= cta < ctas and 0 <= k0 <= max(k0, k1)
+        keys.setdefault((b, group), []).append((k0, k1, cta, place, count))
+        if place < 2:                                     # one result a place
+            assert (cta, place) not in places
+            places.add((cta, place))
+        if count:
+            assert place == 1 and cta not in begun
+            begun[cta] = (b, group, count)
+    assert set(keys) == {(b, g) for b in range(len(lens)) for g in range(heads)}
+    for (b, group), parts in keys.items():
+        n = lens[b] if 0 <= lens[b] <= capacity else 0
+        at = 0
+        for k0, k1, *_ in parts:                          # every key once, in order
+            if k1 > k0:
+                assert k0 == at
+                at = k1
+        assert at == n
+        if len(parts) == 1:
+            assert parts[0][3] == 2 and parts[0][4] == 0
+        else:                                             # neighbouring CTAs, found from the first
+            first = parts[0][2]
+            assert [p[2] for p in parts] == list(range(first, first + len(parts)))
+            assert [p[3] for p in parts] == [1] + [0] * (len(parts) - 1)
+            assert begun[first] == (b, group, len(parts))
+    total = max(1, sum(k1 - k0 for _, _, _, k0, k1, _, _ in pieces if k1 > k0))
+    return pieces, total
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_split_covers_every_key_once(lib, D):
+    r = random.Random(D)
+    _check_split(lib, [0], 1, D, 0, 2)
+    _check_split(lib, [131072], 2, D, 131072, 296)
+    _check_split(lib, [1] * 500, 3, D, 64, 444)
+    _check_split(lib, [-5, 70, 4097, 64], 5, D, 4096, 148)  # refused lengths: one piece without keys
+    _check_split(lib, [1 << 30, 17], 1, D, 1 << 30, 296)    # a list beyond 2^22 places
+    for _ in range(150):
+        B = r.choice([1, 2, 7, 33, 200])
+        longest = r.choice([1, 63, 64, 65, 1000, 20000])
+        lens = [r.choice([0, 1, 64, r.randint(0, longest)]) for _ in range(B)]
+        _check_split(lib, lens, r.choice([1, 2, 8, 12]), D, 20000, r.choice([2, 3, 148, 296, 444]))
+
+
+def test_attn_split_is_even(lib):
+    """No CTA takes more than a unit of keys over the mean of an even batch."""
+    pieces, total = _check_split(lib, [16384] * 16, 2, 256, 16384, 296)
+    work = [0] * 296
+    for cta, _, _, k0, k1, _, _ in pieces:
+        work[cta] += max(0, k1 - k0)
+    assert max(work) <= total / 296 + 64
+
+
+@pytest.mark.parametrize("cluster", [1, 2, 4, 8])
+def test_attn_cluster_covers_every_key_once(lib, cluster):
+    k0, k1 = ctypes.c_int32(), ctypes.c_int32()
+    for n in list(range(0, 300)) + [2047, 2048, 2049, (1 << 30) - 1, 1 << 30]:
+        at = 0
+        for rank in range(cluster):
+            assert lib.gdn_testing_attn_cluster(n, cluster, rank, ctypes.byref(k0), ctypes.byref(k1)) == 0
+            assert k0.value <= k1.value <= n
+            if k1.value > k0.value:
+                assert k0.value == at and k0.value % 16 == 0
+                at = k1.value
+        assert at == n
+
+
+def test_attn_rows_stay_in_the_cache(lib):
+    """The cache row of every key, and -1 for every page outside the cache, whatever the table holds."""
+    r = random.Random(0)
+    for page_size in (1, 2, 7, 16, 17, 24, 64, 100, 1 << 20):
+        P = min(1000, ((1 << 31) - 1) // page_size)
+        pages = [r.choice([0, P - 1, r.randrange(P), -1, P, P + 1, (1 << 31) - 1, -(1 << 31)]) for _ in range(40)]
+        table = (ctypes.c_int32 * 40)(*pages)
+        js = {0, 40 * page_size - 1} | {r.randrange(40 * page_size) for _ in range(300)}
+        js |= {p * page_size + d for p in range(1, 40) for d in (-1, 0)}
+        for j in js:
+            row = lib.gdn_testing_attn_row(table, j, page_size, P)
+            page = pages[j // page_size]
+            assert row == (page * page_size + j % page_size if 0 <= page < P else -1)
+            assert row < P * page_size
