@@ -16,7 +16,7 @@ NVCC_FLAGS = [
     "-O3", "-std=c++17", "-lineinfo",
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-Xcompiler", "-fPIC", "-shared", "-cudart", "shared",
-    "-Xptxas", "-warn-spills",
+    "-Xptxas", "-warn-spills", "--threads", "0",
 ]
 
 
