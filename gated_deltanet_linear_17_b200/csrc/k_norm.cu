@@ -12,12 +12,12 @@
 // columns: the sums are a few shuffles) or a CTA of up to 1024.
 //
 // A row's units are the 16-byte blocks of memory that it touches, so a thread's accesses are aligned
-// whatever the width is: in a row that begins p elements into a block, column c lies at place c + p, and
-// the elements of the first and last block that belong to the neighbouring rows are masked.  (All
-// matrices have the same width and aligned bases, so one p serves all; 8-bit rows begin at a multiple of
-// half a block minus p, and their stores are aligned too.)  kFull: width = 32 L, no masks.  Groups of
-// 128 columns in rows that are not whole blocks fall across the blocks; such rows (kElements) take element
-// accesses: a warp holds the groups, lane l the columns l, l + 32, l + 64, l + 96 of each.
+// whatever the width is.  kFull: width = a thread's columns times L.  kAligned: any whole number of blocks.
+// kShifted: a row begins ph elements into a block, so column c lies at place c + ph, and the elements of the
+// first and last block that belong to the neighbouring rows are masked.  (All matrices have the same width
+// and aligned bases, so one ph serves all; an 8-bit row's blocks are half as long and aligned too.)  A group
+// of 128 columns then begins inside a unit: that unit's lane keeps two maxima, and a row's scales come from
+// shared memory.
 #include <algorithm>
 #include <type_traits>
 
@@ -68,7 +68,7 @@ __device__ __forceinline__ float lanes_max(float x)
     return x;
 }
 
-enum Kind { kFull, kBlocks, kElements };
+enum Kind { kFull, kAligned, kShifted };
 
 // 16 bytes of the activations' type as N fp32 in pairs, and back
 template <class A>
@@ -117,25 +117,25 @@ __host__ __device__ constexpr int norm_block(int L) { return L <= 32 ? kNarrowBl
 template <class A>
 __host__ __device__ constexpr int norm_per(int L) { return sizeof(typename A::raw) == 4 && L <= 512 ? 16 : 32; }
 // CTAs an SM that the registers leave room for
-__host__ __device__ constexpr int norm_ctas(int L) { return (L <= 256 ? 768 : 1024) / norm_block(L); }
+__host__ __device__ constexpr int norm_ctas(int L) { return L <= 256 ? 768 / norm_block(L) : 1024 / L; }
 // Rows up to 8192 columns come through two stages in shared memory: cp.async brings a group's next row while it
 // works on this one.  A thread fetches what it will use itself, so no barrier orders the stages.  Wider rows go
 // straight to registers.
 template <class A>
-__host__ __device__ constexpr bool norm_ring(Kind kind, int L) { return kind != kElements && L * norm_per<A>(L) <= 8192; }
-// Where warps hold whole rows, the weights lie in shared memory in fp32, offset added: in order (kFull), or
-// (kBlocks) as 2 N - 1 lines, line r of the weights r - (N - 1) behind the first of each unit, zeros outside the
+__host__ __device__ constexpr bool norm_ring(int L) { return L * norm_per<A>(L) <= 8192; }
+// Where warps hold whole rows, the weights lie in shared memory in fp32, offset added: in order, or
+// (kShifted) as 2 N - 1 lines, line r of the weights r - (N - 1) behind the first of each unit, zeros outside the
 // row.  A unit of a row that begins ph elements into a block then reads N lines from N - 1 - ph on, its
 // neighbours beside it.
-__host__ __device__ constexpr bool norm_weights(Kind kind, int L) { return kind != kElements && L <= 32; }
+__host__ __device__ constexpr bool norm_weights(int L) { return L <= 32; }
 template <class A>
 __host__ __device__ constexpr int norm_line(int L) { return L * norm_per<A>(L) / Unit<A>::N + 1; }
 template <class A>
 __host__ __device__ constexpr int norm_weight_bytes(Kind kind, int L)
 {
-    return !norm_weights(kind, L) ? 0
-           : kind == kFull        ? L * norm_per<A>(L) * 4
-                                  : ((2 * Unit<A>::N - 1) * norm_line<A>(L) * 4 + 15) / 16 * 16;
+    return !norm_weights(L)   ? 0
+           : kind != kShifted ? L * norm_per<A>(L) * 4
+                              : ((2 * Unit<A>::N - 1) * norm_line<A>(L) * 4 + 15) / 16 * 16;
 }
 __host__ __device__ constexpr int pow2(int n) { return n <= 1 ? 1 : 2 * pow2((n + 1) / 2); }
 
@@ -145,26 +145,31 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
 {
     using U = Unit<A>;
     using raw = typename A::raw;
-    constexpr bool kEl = KIND == kElements, kRing = norm_ring<A>(KIND, L), kShared = norm_weights(KIND, L);
+    constexpr bool kRing = norm_ring<A>(L), kShared = norm_weights(L), kShift = KIND == kShifted;
     constexpr bool kF16 = std::is_same<A, F16>::value;
-    constexpr int N = kEl ? 4 : U::N, H = N / 2, PER = norm_per<A>(L), NV = PER / N;
+    constexpr int N = U::N, H = N / 2, PER = norm_per<A>(L), NV = PER / N;
     constexpr int W = L < 32 ? L : 32, kWarps = pow2(L / 32);  // warps, rounded up for the shuffles
     constexpr int kBlock = norm_block(L), kRows = L <= 32 ? kBlock / L : 1, kStep = L * N;
-    constexpr int kGroupLanes = kEl ? 32 : 128 / N;  // lanes that hold a group of 128 columns
+    constexpr int kGroupLanes = 128 / N;  // lanes that hold a group of 128 columns
     __shared__ float red[2][32];
+    // kShifted, a row's groups: maxima of the elements behind the phase of their first unit, and of those before it
+    // (which belong to the group before)
+    constexpr int kGroups = L * PER / 128 + 1;
+    __shared__ float group_max[kShift ? kRows : 1][kShift ? kGroups : 1], group_lead[kShift ? kRows : 1][kShift ? kGroups : 1];
     extern __shared__ __align__(16) uint8_t smem[];
     begin_early();
     const int t = L <= 32 ? (int)threadIdx.x % L : (int)threadIdx.x;
     const int width = KIND == kFull ? PER * L : p.width, quant = p.quant;
-    const int v0 = kEl ? (t >> 5) * 128 + (t & 31) : t * N;  // place of this thread's first element, phase added
+    const int v0 = t * N;  // place of this thread's first element, phase added
     const int first = (int)(L <= 32 ? blockIdx.x * kRows + threadIdx.x / L : blockIdx.x);
     const int stride = (int)gridDim.x * kRows, rows = (int)p.rows;
+    const int mine_row = L <= 32 ? (int)threadIdx.x / L : 0, groups = (width + GDN_QUANT_GROUP - 1) / GDN_QUANT_GROUP;
     const bool residual = p.residual != nullptr, gated = p.gate != nullptr;
     const raw *x = static_cast<const raw *>(p.x), *res = static_cast<const raw *>(p.residual),
               *gate = static_cast<const raw *>(p.gate);
     const long long end = p.rows * width;
     // elements of the row's first block before the row
-    auto phase = [&](int row) { return KIND == kBlocks ? (int)((long long)row * width) & (N - 1) : 0; };
+    auto phase = [&](int row) { return kShift ? (int)((long long)row * width) & (N - 1) : 0; };
 
     float *weights = reinterpret_cast<float *>(smem);
     uint8_t *ring = smem + norm_weight_bytes<A>(KIND, L);
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     auto rest_of = [&](int row) { return (int)min(end - (long long)row * width, 1LL << 20); };
     auto fetch = [&](int stage, int row) {
         if (row < rows) {
-            const int c0 = v0 - phase(row), rest = KIND == kFull ? 0 : rest_of(row);
+            const int c0 = v0 - phase(row), rest = kShift ? rest_of(row) : 0;
             const long long at = (long long)row * width + c0;
             const raw *fx = x + at, *fr = res + at, *fg = gate + at;
             const uint32_t dst = mine_addr + stage * stage_bytes;
@@ -186,7 +191,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             for (int k = 0; k < NV; ++k) {
                 const int c = c0 + k * kStep;
                 if (KIND != kFull && c >= width) continue;
-                const int bytes = KIND == kFull ? 16 : min(16, (rest - c) * (int)sizeof(raw));
+                const int bytes = !kShift ? 16 : min(16, (rest - c) * (int)sizeof(raw));
                 cp_async16_part(dst + k * kPlane, fx + k * kStep, bytes);
                 if (residual) cp_async16_part(dst + kMatrix + k * kPlane, fr + k * kStep, bytes);
                 if (gated) cp_async16_part(dst + gate_at + k * kPlane, fg + k * kStep, bytes);
@@ -197,49 +202,24 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     // Units from here on: m points at the unit's first element, c is its column, `in` whether the whole unit lies
     // in the row.
     auto load = [&](const raw *m, int c, int rest) {  // without a ring
-        if constexpr (kEl) {
-            uint32_t w[4];
+        if (!kShift || c + N <= rest) return *reinterpret_cast<const uint4 *>(m);
+        uint32_t w[4] = {};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[j] = 0;
-                if (c + 32 * j < width) {
-                    if constexpr (sizeof(raw) == 2) w[j] = __float_as_uint(A::up(m[32 * j]));
-                    else w[j] = __float_as_uint(m[32 * j]);
-                }
+        for (int j = 0; j < N; ++j)
+            if (c + j < rest) {
+                if constexpr (sizeof(raw) == 2) w[j / 2] |= (uint32_t)m[j] << 16 * (j & 1);
+                else w[j] = __float_as_uint(m[j]);
             }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-            if (KIND == kFull || c + N <= rest) return *reinterpret_cast<const uint4 *>(m);
-            uint32_t w[4] = {};
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (c + j < rest) {
-                    if constexpr (sizeof(raw) == 2) w[j / 2] |= (uint32_t)m[j] << 16 * (j & 1);
-                    else w[j] = __float_as_uint(m[j]);
-                }
-            return make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    };
-    auto up = [&](const uint4 &w, float2 (&v)[H]) {
-        if constexpr (kEl) {
-            v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
-            v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
-        } else {
-            U::up(w, v);
-        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
     };
     auto mask = [&](int c, bool in, float2 (&v)[H]) {  // clears what is not in the row
-        if (KIND != kBlocks || in) return;
+        if (!kShift || in) return;
 #pragma unroll
         for (int j = 0; j < N; ++j)
             if ((unsigned)(c + j) >= (unsigned)width) (j & 1 ? v[j / 2].y : v[j / 2].x) = 0.f;
     };
     auto store = [&](raw *m, int c, bool in, const float2 (&v)[H]) {
-        if constexpr (kEl) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + 32 * j < width) m[32 * j] = A::down(j & 1 ? v[j / 2].y : v[j / 2].x);
-        } else if (KIND == kFull || in) {
+        if (!kShift || in) {
             *reinterpret_cast<uint4 *>(m) = U::down(v);
         } else {
 #pragma unroll
@@ -248,11 +228,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         }
     };
     auto store8 = [&](uint8_t *m, int c, bool in, const float2 (&v)[H]) {
-        if constexpr (kEl) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (c + 32 * j < width) m[32 * j] = to_e4m3(j & 1 ? v[j / 2].y : v[j / 2].x);
-        } else if (KIND == kFull || in) {
+        if (!kShift || in) {
             U::store8(m, v);
         } else {
 #pragma unroll
@@ -261,7 +237,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         }
     };
     auto weigh = [&](int k, int c, int ph, bool in, float2 (&w)[H]) {  // the weights of unit k
-        if constexpr (kShared && KIND == kFull) {
+        if constexpr (kShared && !kShift) {
 #pragma unroll
             for (int i = 0; i < N / 4; ++i) {
                 const float4 v = reinterpret_cast<const float4 *>(weights + c)[i];
@@ -275,10 +251,10 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             for (int j = 0; j < H; ++j) w[j] = make_float2(line[2 * j * kLine], line[(2 * j + 1) * kLine]);
             return;
         }
-        if (!kEl && (KIND == kFull || in)) {
+        if (!kShift || in) {
             if (p.weight_f32) {
                 const float *m = static_cast<const float *>(p.weight) + c;
-                if (KIND == kFull || (c & 3) == 0) {
+                if (!kShift || (c & 3) == 0) {
 #pragma unroll
                     for (int i = 0; i < N / 4; ++i) {
                         const float4 v = reinterpret_cast<const float4 *>(m)[i];
@@ -289,8 +265,8 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
 #pragma unroll
                     for (int j = 0; j < H; ++j) w[j] = make_float2(m[2 * j], m[2 * j + 1]);
                 }
-            } else if (KIND == kFull || (c & (N - 1)) == 0) {
-                up(*reinterpret_cast<const uint4 *>(static_cast<const raw *>(p.weight) + c), w);
+            } else if (!kShift || (c & (N - 1)) == 0) {
+                U::up(*reinterpret_cast<const uint4 *>(static_cast<const raw *>(p.weight) + c), w);
             } else {
                 const raw *m = static_cast<const raw *>(p.weight) + c;
 #pragma unroll
@@ -299,8 +275,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const int cc = kEl ? c + 32 * j : c + j;
-                const float f = cc >= 0 && cc < width ? weight_at(p, cc, kF16) : 0.f;
+                const float f = (unsigned)(c + j) < (unsigned)width ? weight_at(p, c + j, kF16) : 0.f;
                 (j & 1 ? w[j / 2].y : w[j / 2].x) = f;
             }
         }
@@ -314,7 +289,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     const int turns = warp_first >= rows ? 0 : (rows - 1 - warp_first) / stride + 1;
     if (kRing) fetch(0, first);
     if (kShared) {
-        if (KIND == kFull) {
+        if (!kShift) {
             for (int c = threadIdx.x; c < width; c += kBlock) weights[c] = weight_at(p, c, kF16) + p.weight_offset;
         } else {
             for (int i = threadIdx.x; i < (2 * N - 1) * kLine; i += kBlock) {
@@ -323,6 +298,9 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             }
         }
     }
+    if (kShift) {
+        for (int i = threadIdx.x; i < kRows * kGroups; i += kBlock) group_max[0][i] = group_lead[0][i] = 0.f;
+    }
     if (kShared || L > 32) {
         if (threadIdx.x < 64) red[threadIdx.x / 32][threadIdx.x % 32] = 0.f;  // for warps that there are not
         __syncthreads();
@@ -330,7 +308,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     for (int turn = 0; turn < turns; ++turn) {
         const int row = first + turn * stride;
         const bool live = row < rows;
-        const int ph = phase(row), c0 = v0 - ph, rest = KIND == kFull ? 0 : rest_of(row);
+        const int ph = phase(row), c0 = v0 - ph, rest = kShift ? rest_of(row) : 0;
         const long long at = (long long)row * width + c0;
         const raw *rx = x + at, *rr = res + at, *rg = gate + at;
         const uint8_t *held = mine + (turn & 1) * stage_bytes;
@@ -339,9 +317,9 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             cp_async_wait<1>();
         }
         auto has = [&](int k) {
-            return live && (KIND == kFull || (kEl ? c0 - (t & 31) : c0) + k * kStep < width);
+            return live && (KIND == kFull || c0 + k * kStep < width);
         };
-        auto inside = [&](int c) { return KIND == kFull || (c >= 0 && c + N <= width); };
+        auto inside = [&](int c) { return !kShift || (c >= 0 && c + N <= width); };
         float2 z[NV][H], sum2 = make_float2(0.f, 0.f);
         constexpr int kBatch = kRing ? 1 : NV / 2;  // units in flight at a time where there is no ring
 #pragma unroll
@@ -362,11 +340,11 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 if (!has(k)) continue;
                 const bool in = inside(c);
                 if (kRing) xw[i] = *reinterpret_cast<const uint4 *>(held + k * kPlane);
-                up(xw[i], z[k]);
+                U::up(xw[i], z[k]);
                 if (residual) {
                     float2 r[H];
                     if (kRing) rw[i] = *reinterpret_cast<const uint4 *>(held + kMatrix + k * kPlane);
-                    up(rw[i], r);
+                    U::up(rw[i], r);
 #pragma unroll
                     for (int j = 0; j < H; ++j) z[k][j] = fadd2(z[k][j], r[j]);
                     store(static_cast<raw *>(p.residual_out) + at + k * kStep, c, in, z[k]);
@@ -384,13 +362,14 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         }
         const float rstd = rsqrtf(fmaf(sum, p.inv_width, p.eps));
 
+        const bool leads = (t & (kGroupLanes - 1)) == 0;  // whether this thread's units begin groups
         float most = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            if (KIND != kFull && k * kStep - (N - 1) >= width) break;  // no thread has such a unit
+            if (KIND != kFull && k * kStep - (kShift ? N - 1 : 0) >= width) break;  // no thread has such a unit
             const int c = c0 + k * kStep;
             const bool in = inside(c);
-            float m = 0.f;
+            float m = 0.f, lead = 0.f;
             if (has(k)) {
                 float2 w[H];
                 weigh(k, c, ph, in, w);
@@ -398,7 +377,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 for (int j = 0; j < H; ++j) z[k][j] = fmul2(fmul2(z[k][j], make_float2(rstd, rstd)), w[j]);
                 if (gated) {
                     float2 g[H];
-                    up(kRing ? *reinterpret_cast<const uint4 *>(held + gate_at + k * kPlane) : load(rg + k * kStep, c, rest), g);
+                    U::up(kRing ? *reinterpret_cast<const uint4 *>(held + gate_at + k * kPlane) : load(rg + k * kStep, c, rest), g);
                     mask(c, in, g);
 #pragma unroll
                     for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], silu(g[j]));
@@ -407,25 +386,47 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 else {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        // past the row's end a NaN of rstd must not reach a group's maximum
-                        if (kEl && c + 32 * j >= width) continue;
-                        m = absmax_nan(m, j & 1 ? z[k][j / 2].y : z[k][j / 2].x);
+                        const float f = j & 1 ? z[k][j / 2].y : z[k][j / 2].x;
+                        if (kShift && leads && j < ph) lead = absmax_nan(lead, f);
+                        else m = absmax_nan(m, f);
                     }
                 }
             }
             if (quant == GDN_QUANT_BLOCK) {
                 m = lanes_max<kGroupLanes < W ? kGroupLanes : W>(m);
-                const float scale = absmax_nan(kMinScale, m * (1.f / kE4m3Max)), inv = __fdividef(1.f, scale);
-                if (has(k)) {
+                if (kShift) {
+                    if (leads) group_max[mine_row][(t + k * L) / kGroupLanes] = m, group_lead[mine_row][(t + k * L) / kGroupLanes] = lead;
+                } else {
+                    const float scale = absmax_nan(kMinScale, m * (1.f / kE4m3Max)), inv = __fdividef(1.f, scale);
+                    if (has(k)) {
 #pragma unroll
-                    for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], make_float2(inv, inv));
-                    store8(static_cast<uint8_t *>(p.out) + at + k * kStep, c, in, z[k]);
-                    if ((t & (kGroupLanes - 1)) == 0)
-                        p.scales[(long long)row * ((width + GDN_QUANT_GROUP - 1) / GDN_QUANT_GROUP) +
-                                 c / GDN_QUANT_GROUP] = scale;
+                        for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], make_float2(inv, inv));
+                        store8(static_cast<uint8_t *>(p.out) + at + k * kStep, c, in, z[k]);
+                        if (leads) p.scales[(long long)row * groups + c / GDN_QUANT_GROUP] = scale;
+                    }
                 }
             }
-            most = absmax_nan(most, m);
+            most = absmax_nan(absmax_nan(most, m), lead);
+        }
+        if (kShift && quant == GDN_QUANT_BLOCK) {
+            if (L > 32) __syncthreads();
+            else __syncwarp();
+            auto scale_of = [&](int g) {
+                return absmax_nan(kMinScale, absmax_nan(group_max[mine_row][g], group_lead[mine_row][g + 1]) * (1.f / kE4m3Max));
+            };
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (!has(k)) continue;
+                const int c = c0 + k * kStep, g = (t + k * L) / kGroupLanes;
+                // (the phase may leave the row's last unit nothing behind it)
+                const float scale = g < groups ? scale_of(g) : kMinScale, inv = __fdividef(1.f, scale);
+                if (leads && g < groups) p.scales[(long long)row * groups + g] = scale;
+                const float before = leads && ph > 0 && g > 0 ? __fdividef(1.f, scale_of(g - 1)) : inv;
+#pragma unroll
+                for (int j = 0; j < N; ++j) (j & 1 ? z[k][j / 2].y : z[k][j / 2].x) *= leads && j < ph ? before : inv;
+                store8(static_cast<uint8_t *>(p.out) + at + k * kStep, c, inside(c), z[k]);
+            }
+            if (L <= 32) __syncwarp();  // (L > 32: the barrier below) before the next row's maxima
         }
         if (quant == GDN_QUANT_ROW) {
             most = lanes_max<W>(most);
@@ -457,7 +458,7 @@ cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
     constexpr int block = norm_block(L), rows = L <= 32 ? block / L : 1;
     const int matrices = 1 + (p.residual != nullptr) + (p.gate != nullptr);
     const size_t smem = norm_weight_bytes<A>(KIND, L) +
-                        (norm_ring<A>(KIND, L) ? (size_t)2 * block * norm_per<A>(L) * sizeof(typename A::raw) * matrices : 0);
+                        (norm_ring<A>(L) ? (size_t)2 * block * norm_per<A>(L) * sizeof(typename A::raw) * matrices : 0);
     if (smem > 47 * 1024) {  // 48 KB with the static part
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -486,13 +487,12 @@ cudaError_t launch_type(NormParams p, cudaStream_t st)
     if (width % N == 0) {
         int lanes = std::max(4, least);
         while (lanes * norm_per<A>(lanes) < width) lanes *= 2;
-        return lanes * norm_per<A>(lanes) == width ? launch_lanes<A, kFull, 4, 8, 16, 32, 64, 128, 256, 512, 1024>(p, width, least, st)
-                    : launch_lanes<A, kBlocks, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width, least, st);
+        return lanes * norm_per<A>(lanes) == width
+                   ? launch_lanes<A, kFull, 4, 8, 16, 32, 64, 128, 256, 512, 1024>(p, width, least, st)
+                   : launch_lanes<A, kAligned, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 320, 384, 512, 1024>(p, width, least, st);
     }
-    if (p.quant == GDN_QUANT_BLOCK) return launch_lanes<A, kElements, 32, 128, 512, 1024>(p, width, 0, st);
-    // a row that begins inside a block may take a unit more; the widest do not find room for it
-    if (width + N - 1 > GDN_NORM_MAX_WIDTH) return launch_lanes<A, kElements, 1024>(p, width, 0, st);
-    return launch_lanes<A, kBlocks, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width + N - 1, 0, st);
+    // a row that begins inside a block takes up to a unit more
+    return launch_lanes<A, kShifted, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width + N - 1, least, st);
 }
 
 }  // namespace

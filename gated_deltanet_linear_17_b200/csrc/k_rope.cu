@@ -183,7 +183,10 @@ cudaError_t launch_dim(const RopeParams &p, cudaStream_t st)
     const size_t smem = sizeof(float2) * tokens * ((p.n + 1) & ~1);
     switch (p.D) {
     case 64: return launch_early(rope_kernel<A, LAYOUT, 64>, grid, kRopeThreads, smem, st, p);
+    case 80: return launch_early(rope_kernel<A, LAYOUT, 80>, grid, kRopeThreads, smem, st, p);
+    case 96: return launch_early(rope_kernel<A, LAYOUT, 96>, grid, kRopeThreads, smem, st, p);
     case 128: return launch_early(rope_kernel<A, LAYOUT, 128>, grid, kRopeThreads, smem, st, p);
+    case 192: return launch_early(rope_kernel<A, LAYOUT, 192>, grid, kRopeThreads, smem, st, p);
     case 256: return launch_early(rope_kernel<A, LAYOUT, 256>, grid, kRopeThreads, smem, st, p);
     default: return launch_early(rope_kernel<A, LAYOUT, 0>, grid, kRopeThreads, smem, st, p);
     }

@@ -63,7 +63,8 @@ extern "C" {
  *   residual_out  [rows, width] of act_dtype; may be residual itself
  *   scales        fp32 [rows] or [rows, ceil(width / GDN_QUANT_GROUP)]; NULL
  *                 without an 8-bit output
- *   rows          >= 0 (0 is a no-op); width 1 .. GDN_NORM_MAX_WIDTH
+ *   rows          >= 0 (0 is a no-op); width 1 .. GDN_NORM_MAX_WIDTH, at most
+ *                 GDN_NORM_MAX_WIDTH - 8 where it is no multiple of 8
  * A row that holds a NaN or an infinity in z comes out as NaN where the formula
  * gives NaN.  |z| from about 1.8e19 on overflows the fp32 mean and the row
  * comes out as zero.

@@ -114,7 +114,7 @@ def check_norm(x, w, residual=None, gate=None, quant=None, eps=1e-6, offset=0.0)
 
 
 WIDTHS = [1, 2, 7, 8, 64, 72, 120, 127, 128, 129, 136, 256, 257, 320, 1000, 1024, 1032, 1537, 2048, 4096, 5001, 8192,
-          8193, 8200, 11111, 16384, 32760, 32768, 32767]
+          8193, 8200, 10240, 11111, 16384, 32759, 32760, 32768]
 
 
 @pytest.mark.parametrize("width", WIDTHS)

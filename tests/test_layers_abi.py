@@ -45,6 +45,8 @@ def _norm(lib, **over):
     (dict(quant=-1), B.GDN_ERR_BAD_SHAPE),
     (dict(act=1, wdt=2), B.GDN_ERR_BAD_SHAPE),               # a weight in the other 16-bit type
     (dict(width=32769), B.GDN_ERR_UNSUPPORTED),
+    (dict(width=32776), B.GDN_ERR_UNSUPPORTED),
+    (dict(width=32761), B.GDN_ERR_UNSUPPORTED),               # no whole number of blocks, and no room for one more
     (dict(rows=1 << 31), B.GDN_ERR_UNSUPPORTED),
     (dict(rows=0), B.GDN_OK),
     (dict(rows=0, x=None), B.GDN_OK),
