@@ -23,7 +23,7 @@
 // Inside a CTA four warps take every fourth tile of 16 keys.  A warp is on its own until the end of the
 // piece: its own ring of tiles in shared memory, filled by cp.async a few tiles ahead, its own running
 // maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end of a piece the
-// four partial results are joined through shared memory.
+// four partial results are joined through shared memory, while the next piece's tiles are on their way.
 //
 // Roundings.  Scores, exponentials (base 2, the scale folded in), sums and outputs are fp32.  The
 // probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
@@ -56,9 +56,7 @@ struct Shape {
     static constexpr int kQ = kRows * D * 2;         // query rows, behind the rings
     static constexpr int kSmem = kWarps * kRing + kQ;
     static constexpr bool kQInRegs = D * NT < 512;   // query fragments stay in registers
-    static constexpr int kSum = D + 4;               // floats of a row in the join of the warps: the four rows that
-                                                     // a quad writes lie 8 banks apart
-    static_assert(kWarps * kRing >= kWarps * kRows * kSum * 4, "the join of the warps fits into the rings");
+    static_assert(kStage >= kRows * D * 4, "a warp's sums fit into a stage");
 };
 
 // byte offset of 16-byte chunk c of row r in a tile of D-element rows: eight rows at one chunk lie in
@@ -186,121 +184,167 @@ __device__ __forceinline__ void write_out(const AttnParams &p, long long head, i
     if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
 }
 
-// DIRECT: a cluster of p.direct CTAs a pair
+// One piece of a CTA's work: keys [k0, k1) of head group `pair` of sequence b (of the list, `take` places from u0
+// on), and how many places of the CTA's part lie behind it.
+struct Piece {
+    int b, pair, n, n_next;  // n: the sequence's length as given, n_next: of the sequence behind it
+    int u0, take, k0, k1;
+    long long left;
+};
+template <int D>
+__device__ __forceinline__ void cut(Piece &c, const AttnParams &p)  // the piece that begins at u0
+{
+    c.take = (int)min(c.left, (long long)(attn_places(D, c.n, p.capacity) - c.u0));
+    c.left -= c.take;
+    const KeyRange k = attn_keys(D, c.u0, c.take, attn_refused(c.n, p.capacity) ? 0 : c.n);
+    c.k0 = k.k0;
+    c.k1 = k.k1;
+}
+template <int D>
+__device__ __forceinline__ void next_piece(Piece &c, const AttnParams &p, int heads)
+{
+    c.u0 = 0;
+    if (++c.pair == heads) {
+        c.pair = 0;
+        ++c.b;
+        c.n = c.n_next;
+        c.n_next = c.b + 1 < p.B ? p.lens[c.b + 1] : 0;
+    }
+    cut<D>(c, p);
+}
+
+// DIRECT: a cluster of p.direct CTAs a pair, one piece a CTA.  Otherwise the pieces of the CTA's part of the list, one
+// behind the other: a warp's ring runs on over their borders (it fetches the next piece's tiles while it works on
+// this one's), and only the join of the warps at a piece's end stops the CTA.
 template <int D, int NT, bool F16, bool DIRECT>
 __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, DIRECT>::kCtas)
     paged_attn_kernel(const AttnParams p)
 {
     using S = Shape<D, NT, DIRECT>;
-    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
+    __shared__ int wslot[kWarps];     // the stage that holds a warp's sums while the warps are joined
     __shared__ float2 joined[kRows];  // DIRECT: maximum and sum of this CTA's part of the keys
     begin_early();
+    if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's small CTAs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t ring = smem_addr(smem) + warp * S::kRing;
     const uint32_t qs = smem_addr(smem) + kWarps * S::kRing;
     const uint16_t *kc = static_cast<const uint16_t *>(p.k), *vc = static_cast<const uint16_t *>(p.v);
     const int heads = p.Hkv * p.row_tiles;
 
-    int b, pair, n_raw;
-    // the list: this CTA's part of it, the places of a pair of sequence b, and the first place of the piece at hand
+    Piece now;
     Part part = {};
-    long long left_places = 0, pos = 0;
-    int u_all = 0, u0 = 0;
-    int4 begun = make_int4(0, 0, 0, 0);
     const int rank = DIRECT ? (int)blockIdx.x % p.direct : 0;
     if (DIRECT) {
         const int at = (int)blockIdx.x / p.direct;
-        b = at / heads;
-        pair = at - b * heads;
-        n_raw = p.lens[b];
+        now.b = at / heads;
+        now.pair = at - now.b * heads;
+        now.n = p.lens[now.b];
+        const KeyRange k = attn_cluster_keys(rank, p.direct, attn_refused(now.n, p.capacity) ? 0 : now.n);
+        now.k0 = k.k0;
+        now.k1 = k.k1;
+        now.left = now.n_next = now.u0 = now.take = 0;
     } else {
         part = find_part<D, kThreads>(p);
         if ((int)blockIdx.x >= part.ctas) {
-            if (tid == 0) p.begun[blockIdx.x] = begun;
+            if (tid == 0) p.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
             return;
         }
-        left_places = part.last - part.first;
-        pos = part.first;
-        b = part.b;
-        n_raw = part.n;
-        u_all = attn_places(D, n_raw, p.capacity);
-        pair = part.pair;
-        u0 = part.u0;
+        now.b = part.b;
+        now.pair = part.pair;
+        now.n = part.n;
+        now.n_next = now.b + 1 < p.B ? p.lens[now.b + 1] : 0;
+        now.u0 = part.u0;
+        now.left = part.last - part.first;
+        cut<D>(now, p);
     }
 
-    for (;;) {
-    // this piece: keys [k0, k1) of head group `pair` of sequence b; of the list, places [u0, u0 + take)
-    const int take = DIRECT ? 0 : (int)min(left_places, (long long)(u_all - u0));
-    const bool whole = DIRECT ? p.direct == 1 : take == u_all;
-    const bool bad = attn_refused(n_raw, p.capacity);
-    const int n = bad ? 0 : n_raw;
-    const int hkv = pair / p.row_tiles, tile_row0 = (pair - hkv * p.row_tiles) * kRows;
-    const int rows = min(kRows, p.group - tile_row0);
-    const int head0 = hkv * p.group + tile_row0;  // first query head of this piece
-    const KeyRange keys = DIRECT ? attn_cluster_keys(rank, p.direct, n) : attn_keys(D, u0, take, n);
-    const int k0 = keys.k0, k1 = keys.k1;
-    const int n_next = !DIRECT && b + 1 < p.B ? p.lens[b + 1] : 0;
-
-    // this warp's tiles: first + 16 (warp + 4 i)
-    const int tiles = (k1 - k0 + kTile - 1) / kTile;
-    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    const int32_t *table = p.table + (long long)b * p.max_pages;
-    bool bad_page = false;
-    // cache row of key (lane & 15) of tile i; -1 past the piece or on a page outside the cache
-    auto cache_row = [&](int i) {
-        const int j = k0 + kTile * (warp + kWarps * i) + (lane & 15);
-        if (i >= mine || j >= k1) return -1;
-        const int row = attn_cache_row(table, j, p.by_page, p.page_size, p.P);
-        bad_page |= row < 0;
-        return row;
+    // this warp's tiles of a piece: those at k0 + 16 (warp + kWarps i)
+    auto tiles_of = [&](const Piece &c) {
+        const int tiles = (c.k1 - c.k0 + kTile - 1) / kTile;
+        return tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
     };
-    auto fetch = [&](int stage, int row) {
-        const uint32_t dst = ring + stage * S::kStage;
+    // The next tile to be looked up: the i-th of piece `ahead`, of which this warp has `count`.
+    Piece ahead = now;
+    int i_ahead = 0, count = tiles_of(ahead);
+    // A tile to be fetched: the cache row of its key (lane % 16), -1 behind the piece's last key, -2 on a page outside
+    // the cache; and its head, or -1 when there is none left.  It is looked up a tile ahead of its use.
+    struct Tile {
+        int row, hkv;
+    };
+    auto look_up = [&]() {
+        while (i_ahead >= count && ahead.left > 0) {
+            next_piece<D>(ahead, p, heads);
+            i_ahead = 0;
+            count = tiles_of(ahead);
+        }
+        Tile t = {-1, -1};
+        if (i_ahead >= count) return t;
+        t.hkv = ahead.pair / p.row_tiles;
+        const int j = ahead.k0 + kTile * (warp + kWarps * i_ahead) + (lane & 15);
+        if (j < ahead.k1) {
+            t.row = attn_cache_row(p.table + (long long)ahead.b * p.max_pages, j, p.by_page, p.page_size, p.P);
+            if (t.row < 0) t.row = -2;
+        }
+        ++i_ahead;
+        return t;
+    };
+    uint32_t bad_pages = 0;  // a bit for each stage whose tile has one
+    auto fetch = [&](int stage, const Tile &t) {
+        if (t.hkv >= 0) {
+            const uint32_t dst = ring + stage * S::kStage;
 #pragma unroll
-        for (int i = 0; i < kTile * (D / 8) / 32; ++i) {
-            const int id = lane + 32 * i, r = id / (D / 8), c = id % (D / 8);
-            const int rr = __shfl_sync(0xffffffffu, row, r);
-            const long long at = rr < 0 ? 0 : ((long long)rr * p.Hkv + hkv) * D + 8 * c;
-            cp_async16(dst + sw<D>(r, c), kc + at, rr >= 0);
-            cp_async16(dst + S::kHalf + sw<D>(r, c), vc + at, rr >= 0);
+            for (int i = 0; i < kTile * (D / 8) / 32; ++i) {
+                const int id = lane + 32 * i, r = id / (D / 8), c = id % (D / 8);
+                const int rr = __shfl_sync(0xffffffffu, t.row, r);
+                const long long at = rr < 0 ? 0 : ((long long)rr * p.Hkv + t.hkv) * D + 8 * c;
+                cp_async16(dst + sw<D>(r, c), kc + at, rr >= 0);
+                cp_async16(dst + S::kHalf + sw<D>(r, c), vc + at, rr >= 0);
+            }
+            const uint32_t bad = __any_sync(0xffffffffu, t.row == -2);
+            bad_pages = (bad_pages & ~(1u << stage)) | bad << stage;
+        }
+        cp_async_commit();
+    };
+    // A thread's 16-byte parts of a piece's query rows (rows past the group's zero)
+    constexpr int kParts = (kRows * (D / 8) + kThreads - 1) / kThreads;
+    auto read_queries = [&](uint4 (&x)[kParts], const Piece &c) {
+        const int hkv = c.pair / p.row_tiles, row0 = (c.pair - hkv * p.row_tiles) * kRows;
+        const uint16_t *q = static_cast<const uint16_t *>(p.q) + ((long long)c.b * p.Hq + hkv * p.group + row0) * D;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int id = tid + i * kThreads, r = id / (D / 8), ch = id % (D / 8);
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < min(kRows, p.group - row0)) x[i] = reinterpret_cast<const uint4 *>(q + (long long)r * D)[ch];
+        }
+    };
+    auto keep_queries = [&](const uint4 (&x)[kParts]) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const int id = tid + i * kThreads, r = id / (D / 8), ch = id % (D / 8);
+            if (r < kRows) *reinterpret_cast<uint4 *>(smem + kWarps * S::kRing + sw<D>(r, ch)) = x[i];
         }
     };
 
     // the first tiles are on their way before the queries are waited for
+    Tile tile;
     {
-        int row[S::kStages - 1];
+        Tile t[kStages - 1];
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) row[i] = cache_row(i);
+        for (int i = 0; i < kStages - 1; ++i) t[i] = look_up();
+        tile = look_up();
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) {
-            if (i < mine) fetch(i, row[i]);
-            cp_async_commit();
-        }
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, t[i]);
     }
-    int next_row = cache_row(S::kStages - 1);
-    // query rows to shared memory (rows past the group's zero)
-    for (int i = tid; i < kRows * (D / 8); i += kThreads) {
-        const int r = i / (D / 8), c = i % (D / 8);
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows)
-            x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) +
-                                                ((long long)b * p.Hq + head0 + r) * D)[c];
-        *reinterpret_cast<uint4 *>(smem + kWarps * S::kRing + sw<D>(r, c)) = x;
+    {
+        uint4 x[kParts];
+        read_queries(x, now);
+        keep_queries(x);
     }
     __syncthreads();
 
-    // o: the output transposed, o[t][r][e] at column 16 t + lane / 4 (+ 8 for e >= 2) of query row 8 r + 2 (lane % 4)
-    // (+ 1 for odd e); m, l: of query row 8 r + lane / 4 (l this lane's part of the sum)
-    float o[D / 16][NT][4], m[NT], l[NT];
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) o[t][r][0] = o[t][r][1] = o[t][r][2] = o[t][r][3] = 0.f;
-    }
     auto query = [&](int k, uint32_t (&a)[4]) {  // 16 columns of the query rows (rows 8 .. 15 zero when NT is 1)
         if (NT == 2) ldsm_x4(qs + sw<D>(lane & 15, 2 * k + (lane >> 4)), a[0], a[1], a[2], a[3]);
         else {
@@ -308,204 +352,232 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             a[1] = a[3] = 0;
         }
     };
-    uint32_t qf[S::kQInRegs ? D / 16 : 1][4];
-    if (S::kQInRegs) {
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) query(k, qf[k]);
-    }
 
-    int stage = 0;
-    for (int i = 0; i < mine; ++i) {
-        cp_async_wait<S::kStages - 2>();
-        __syncwarp();
-        {
-            const int ahead = i + S::kStages - 1;
-            if (ahead < mine) fetch(stage == 0 ? S::kStages - 1 : stage - 1, next_row);
-            cp_async_commit();
-            next_row = cache_row(ahead + 1);
-        }
-        const uint32_t ks = ring + stage * S::kStage, vs = ks + S::kHalf;
-        stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    long long pos = part.first;  // of the list: the piece's first place
+    int4 begun = make_int4(0, 0, 0, 0);
+    int stage = 0;  // of this warp's next tile; the one before it is free
+    for (;;) {
+        const int hkv = now.pair / p.row_tiles, row0 = (now.pair - hkv * p.row_tiles) * kRows;
+        const int rows = min(kRows, p.group - row0), head0 = hkv * p.group + row0;
+        const int all = DIRECT ? 0 : attn_places(D, now.n, p.capacity);
+        const bool whole = DIRECT ? p.direct == 1 : now.take == all;
 
-        // scores of the query rows against 16 keys; even and odd steps apart, to halve the chain of additions
-        float s[2][4] = {}, s1[2][4] = {};
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            uint32_t b0, b1, b2, b3;
-            ldsm_x4(ks + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b0, b1, b2, b3);
-            if (!S::kQInRegs) query(k, qf[0]);
-            const uint32_t *a = qf[S::kQInRegs ? k : 0];
-            mma<F16>(k & 1 ? s1[0] : s[0], a, b0, b1);
-            mma<F16>(k & 1 ? s1[1] : s[1], a, b2, b3);
-        }
-        const int left = k1 - (k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. 16, or more)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 2 * NT; ++e) {
-                const int key = 8 * t + 2 * (lane & 3) + (e & 1);
-                s[t][e] = key < left ? (s[t][e] + s1[t][e]) * p.scale_log2 : -INFINITY;
-            }
-        float alpha[NT], ref[NT];
-        bool moved = false;
+        // o: the output transposed, o[t][r][e] at column 16 t + lane / 4 (+ 8 for e >= 2) of query row
+        // 8 r + 2 (lane % 4) (+ 1 for odd e); m, l: of query row 8 r + lane / 4 (l this lane's part of the sum)
+        float o[D / 16][NT][4], m[NT], l[NT];
 #pragma unroll
         for (int r = 0; r < NT; ++r) {
-            const float top =
-                quad_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])));
-            const float now = fmaxf(m[r], top);
-            ref[r] = now == -INFINITY ? 0.f : now;  // every score -infinity so far: the exponentials are 0
-            alpha[r] = exp2f(m[r] - ref[r]);
-            moved |= alpha[r] != 1.f;
-            m[r] = now;
-            l[r] *= alpha[r];
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) o[t][r][0] = o[t][r][1] = o[t][r][2] = o[t][r][3] = 0.f;
         }
-        if (__any_sync(0xffffffffu, moved)) {
+        uint32_t qf[S::kQInRegs ? D / 16 : 1][4];
+        if (S::kQInRegs) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) query(k, qf[k]);
+        }
+        bool bad = attn_refused(now.n, p.capacity);
+
+        const int mine = tiles_of(now);
+        for (int i = 0; i < mine; ++i) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            fetch(stage == 0 ? kStages - 1 : stage - 1, tile);
+            tile = look_up();
+            const uint32_t ks = ring + stage * S::kStage, vs = ks + S::kHalf;
+            bad |= bad_pages >> stage & 1;
+            stage = stage + 1 == kStages ? 0 : stage + 1;
+
+            // scores of the query rows against 16 keys; even and odd steps apart, to halve the chain of additions
+            float s[2][4] = {}, s1[2][4] = {};
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(ks + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b0, b1, b2, b3);
+                if (!S::kQInRegs) query(k, qf[0]);
+                const uint32_t *a = qf[S::kQInRegs ? k : 0];
+                mma<F16>(k & 1 ? s1[0] : s[0], a, b0, b1);
+                mma<F16>(k & 1 ? s1[1] : s[1], a, b2, b3);
+            }
+            const int left = now.k1 - (now.k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. 16, or more)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 2 * NT; ++e) {
+                    const int key = 8 * t + 2 * (lane & 3) + (e & 1);
+                    s[t][e] = key < left ? (s[t][e] + s1[t][e]) * p.scale_log2 : -INFINITY;
+                }
+            float alpha[NT], ref[NT];
+            bool moved = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
-                const float a0 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3));
-                const float a1 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3) + 4);
+                const float top =
+                    quad_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])));
+                const float most = fmaxf(m[r], top);
+                ref[r] = most == -INFINITY ? 0.f : most;  // every score -infinity so far: the exponentials are 0
+                alpha[r] = exp2f(m[r] - ref[r]);
+                moved |= alpha[r] != 1.f;
+                m[r] = most;
+                l[r] *= alpha[r];
+            }
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int t = 0; t < D / 16; ++t) {
-                    o[t][r][0] *= a0;
-                    o[t][r][1] *= a1;
-                    o[t][r][2] *= a0;
-                    o[t][r][3] *= a1;
+                for (int r = 0; r < NT; ++r) {
+                    const float a0 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3));
+                    const float a1 = __shfl_sync(0xffffffffu, alpha[r], 8 * (lane & 3) + 4);
+#pragma unroll
+                    for (int t = 0; t < D / 16; ++t) {
+                        o[t][r][0] *= a0;
+                        o[t][r][1] *= a1;
+                        o[t][r][2] *= a0;
+                        o[t][r][3] *= a1;
+                    }
                 }
             }
+            // The scores' fragment (query row lane / 4, keys 2 (lane % 4) + ..) is, packed, the second operand of
+            // V^T P^T (its column lane / 4, its rows 2 (lane % 4) + ..): no exchange between lanes.
+            uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+            for (int r = 0; r < NT; ++r)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const float p0 = exp2f(s[t][2 * r] - ref[r]), p1 = exp2f(s[t][2 * r + 1] - ref[r]);
+                    l[r] += p0 + p1;
+                    split2<F16>(p0, p1, hi[r][t], lo[r][t]);
+                }
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) {
+                uint32_t a[4];
+                ldsm_x4_t(vs + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0], a[1], a[2],
+                          a[3]);
+#pragma unroll
+                for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][0], hi[r][1]);
+#pragma unroll
+                for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][0], lo[r][1]);
+            }
         }
-        // The scores' fragment (query row lane / 4, keys 2 (lane % 4) + ..) is, packed, the second operand of
-        // V^T P^T (its column lane / 4, its rows 2 (lane % 4) + ..): no exchange between lanes.
-        uint32_t hi[NT][2], lo[NT][2];
+
+        // The end of the piece: join the warps.  A warp's sums go to its free stage; the next piece's queries are on
+        // their way meanwhile.
+        const bool last = DIRECT || now.left == 0;
+        Piece next = now;
+        uint4 x_next[kParts];
+        if (!last) {
+            next_piece<D>(next, p, heads);
+            read_queries(x_next, next);
+        }
+        if (bad) {
+#pragma unroll
+            for (int r = 0; r < NT; ++r) l[r] = NAN;
+        }
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+            l[r] = quad_sum(l[r]);
+            if ((lane & 3) == 0) {
+                wm[warp][lane / 4 + 8 * r] = m[r];
+                wl[warp][lane / 4 + 8 * r] = l[r];
+            }
+        }
+        // DIRECT: no copy is on its way any more, and the CTAs of a cluster have to agree on the stage
+        const int slot = DIRECT || stage == 0 ? kStages - 1 : stage - 1;
+        if (lane == 0) wslot[warp] = slot;
+        if (DIRECT) cp_async_wait<0>();
+        __syncthreads();
+        // row `row`, column d of a warp's sums lies at row D + (d ^ 8 (row / 2 % 4)): the four rows that a quad writes
+        // fall into different banks
+        auto sums = [&](int w) { return reinterpret_cast<float *>(smem + w * S::kRing + wslot[w] * S::kStage); };
+        auto swizzled = [](int row, int d) { return row * D + (d ^ (((row >> 1) & 3) << 3)); };
+        auto top_of = [&](int row) {
+            float top = wm[0][row];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wm[w][row]);
+            return top == -INFINITY ? 0.f : top;
+        };
+        float *os = sums(warp);
 #pragma unroll
         for (int r = 0; r < NT; ++r)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float p0 = exp2f(s[t][2 * r] - ref[r]), p1 = exp2f(s[t][2 * r + 1] - ref[r]);
-                l[r] += p0 + p1;
-                split2<F16>(p0, p1, hi[r][t], lo[r][t]);
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * r + 2 * (lane & 3) + e;
+                if (row >= rows) continue;
+                const float f = exp2f(wm[warp][row] - top_of(row));
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    os[swizzled(row, 16 * t + lane / 4)] = o[t][r][e] * f;
+                    os[swizzled(row, 16 * t + lane / 4 + 8)] = o[t][r][2 + e] * f;
+                }
             }
+        if (!last) keep_queries(x_next);  // every warp is done with this piece's
+        __syncthreads();
+        for (int i = tid; i < rows * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), c = i % (D / 4), at = swizzled(row, 4 * c);
+            const float top = top_of(row);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) {
-            uint32_t a[4];
-            ldsm_x4_t(vs + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0], a[1], a[2], a[3]);
-#pragma unroll
-            for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][0], hi[r][1]);
-#pragma unroll
-            for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][0], lo[r][1]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float4 y = *reinterpret_cast<const float4 *>(sums(w) + at);
+                x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                sum += wl[w][row] * exp2f(wm[w][row] - top);
+            }
+            if (whole) {
+                write_out<D, F16>(p, (long long)now.b * p.Hq + head0 + row, c, x, top, sum);
+            } else if (DIRECT) {
+                *reinterpret_cast<float4 *>(sums(0) + at) = x;  // where this thread read the first warp's part
+                if (c == 0) joined[row] = make_float2(sum == 0.f ? -INFINITY : top, sum);
+            } else {
+                // place 1: the pair begins here; place 0: it began in an earlier CTA.  A piece without a weight has
+                // no maximum either: its stand-in 0 would drown scores far below it
+                const long long to = (2LL * blockIdx.x + (now.u0 == 0)) * 16 + row;
+                reinterpret_cast<float4 *>(p.part + to * D)[c] = x;
+                if (c == 0) p.part_ml[to] = make_float2(sum == 0.f ? -INFINITY : top, sum);
+            }
         }
+        if (DIRECT) {
+            if (whole) return;
+            cluster_arrive_wait();
+            for (int i = rank * kThreads + tid; i < rows * (D / 4); i += p.direct * kThreads) {
+                const int row = i / (D / 4), c = i % (D / 4);
+                const uint32_t ml = smem_addr(joined + row), xs = smem_addr(sums(0) + swizzled(row, 4 * c));
+                float2 part_ml[kAttnMaxCluster];
+                float4 part_x[kAttnMaxCluster];
+                float top = -INFINITY, sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < kAttnMaxCluster; ++r) {
+                    if (r >= p.direct) break;
+                    part_ml[r] = cluster_load2(in_cta(ml, r));
+                    part_x[r] = cluster_load4(in_cta(xs, r));
+                }
+#pragma unroll
+                for (int r = 0; r < kAttnMaxCluster; ++r)
+                    if (r < p.direct) top = fmaxf(top, part_ml[r].x);
+                top = top == -INFINITY ? 0.f : top;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int r = 0; r < kAttnMaxCluster; ++r) {
+                    if (r >= p.direct) break;
+                    const float w = exp2f(part_ml[r].x - top);
+                    sum = fmaf(w, part_ml[r].y, sum);
+                    x.x = fmaf(w, part_x[r].x, x.x), x.y = fmaf(w, part_x[r].y, x.y);
+                    x.z = fmaf(w, part_x[r].z, x.z), x.w = fmaf(w, part_x[r].w, x.w);
+                }
+                write_out<D, F16>(p, (long long)now.b * p.Hq + head0 + row, c, x, top, sum);
+            }
+            cluster_arrive_wait();  // no CTA leaves while another reads its shared memory
+            return;
+        }
+        if (!whole && now.u0 == 0) {
+            // the CTA that holds the pair's last place
+            const int until = attn_part_of(part.total, pos + all - 1, part.ctas);
+            begun = make_int4(now.b, head0, rows, until - (int)blockIdx.x + 1);
+        }
+        if (last) break;
+        pos += now.take;
+        now = next;
+        __syncthreads();  // the free stages, wm, wl and wslot are free again
     }
     cp_async_wait<0>();
-    if (__any_sync(0xffffffffu, bad_page) || bad) {
-#pragma unroll
-        for (int r = 0; r < NT; ++r) l[r] = NAN;
-    }
-
-    // join the warps
-#pragma unroll
-    for (int r = 0; r < NT; ++r) {
-        l[r] = quad_sum(l[r]);
-        if ((lane & 3) == 0) {
-            wm[warp][lane / 4 + 8 * r] = m[r];
-            wl[warp][lane / 4 + 8 * r] = l[r];
-        }
-    }
-    __syncthreads();  // every warp is done with its ring
-    float *os = reinterpret_cast<float *>(smem);
-    auto top_of = [&](int row) {
-        float top = wm[0][row];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wm[w][row]);
-        return top == -INFINITY ? 0.f : top;
-    };
-#pragma unroll
-    for (int r = 0; r < NT; ++r)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = 8 * r + 2 * (lane & 3) + e;
-            if (row >= rows) continue;
-            const float f = exp2f(wm[warp][row] - top_of(row));
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-                float *at = os + (warp * kRows + row) * S::kSum + 16 * t + lane / 4;
-                at[0] = o[t][r][e] * f;
-                at[8] = o[t][r][2 + e] * f;
-            }
-        }
-    __syncthreads();
-    for (int i = tid; i < rows * (D / 4); i += kThreads) {
-        const int row = i / (D / 4), c = i % (D / 4);
-        const float top = top_of(row);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float4 y = reinterpret_cast<const float4 *>(os + (w * kRows + row) * S::kSum)[c];
-            x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-            sum += wl[w][row] * exp2f(wm[w][row] - top);
-        }
-        if (whole) {
-            write_out<D, F16>(p, (long long)b * p.Hq + head0 + row, c, x, top, sum);
-        } else if (DIRECT) {
-            reinterpret_cast<float4 *>(os + row * S::kSum)[c] = x;  // where this thread read the first warp's part
-            if (c == 0) joined[row] = make_float2(sum == 0.f ? -INFINITY : top, sum);
-        } else {
-            // place 1: the pair begins here; place 0: it began in an earlier CTA.  A piece without a weight has no
-            // maximum either: its stand-in 0 would drown scores far below it
-            const long long at = (2LL * blockIdx.x + (u0 == 0)) * 16 + row;
-            reinterpret_cast<float4 *>(p.part + at * D)[c] = x;
-            if (c == 0) p.part_ml[at] = make_float2(sum == 0.f ? -INFINITY : top, sum);
-        }
-    }
-    if (DIRECT) {
-        if (whole) return;
-        cluster_arrive_wait();
-        for (int i = rank * kThreads + tid; i < rows * (D / 4); i += p.direct * kThreads) {
-            const int row = i / (D / 4), c = i % (D / 4);
-            const uint32_t ml = smem_addr(joined + row), xs = smem_addr(os + row * S::kSum) + 16 * c;
-            float2 part_ml[kAttnMaxCluster];
-            float4 part_x[kAttnMaxCluster];
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int r = 0; r < kAttnMaxCluster; ++r) {
-                if (r >= p.direct) break;
-                part_ml[r] = cluster_load2(in_cta(ml, r));
-                part_x[r] = cluster_load4(in_cta(xs, r));
-            }
-#pragma unroll
-            for (int r = 0; r < kAttnMaxCluster; ++r)
-                if (r < p.direct) top = fmaxf(top, part_ml[r].x);
-            top = top == -INFINITY ? 0.f : top;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int r = 0; r < kAttnMaxCluster; ++r) {
-                if (r >= p.direct) break;
-                const float w = exp2f(part_ml[r].x - top);
-                sum = fmaf(w, part_ml[r].y, sum);
-                x.x = fmaf(w, part_x[r].x, x.x), x.y = fmaf(w, part_x[r].y, x.y);
-                x.z = fmaf(w, part_x[r].z, x.z), x.w = fmaf(w, part_x[r].w, x.w);
-            }
-            write_out<D, F16>(p, (long long)b * p.Hq + head0 + row, c, x, top, sum);
-        }
-        cluster_arrive_wait();  // no CTA leaves while another reads its shared memory
-        return;
-    }
-    if (!whole && u0 == 0) {
-        // the CTA that holds the pair's last place
-        const int until = attn_part_of(part.total, pos + u_all - 1, part.ctas);
-        begun = make_int4(b, head0, rows, until - (int)blockIdx.x + 1);
-    }
-    left_places -= take;
-    if (left_places == 0) break;
-    pos += take;
-    u0 = 0;
-    if (++pair == heads) {
-        pair = 0;
-        ++b;
-        n_raw = n_next;
-        u_all = attn_places(D, n_raw, p.capacity);
-    }
-    __syncthreads();  // the rings, the query rows and wm, wl are free again
-    }
     if (tid == 0) p.begun[blockIdx.x] = begun;
 }
 
@@ -515,7 +587,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 // GPU) one CTA's for each 32 columns, its threads spread over the pieces.  Its CTAs are small enough (8K registers,
 // 13 KB) to lie beside the first kernel's on every SM before that ends; what is left behind its end is then two
 // loads, one waiting for the other.
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtas = kAttnSms, kFewPieces = 4;
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtas = 4 * kAttnSms, kFewPieces = 4;
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const AttnParams p)
@@ -680,20 +752,8 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
         const auto kern = paged_attn_kernel<D, NT, F16, true>;
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3((unsigned)(p.B * p.Hkv * p.row_tiles * p.direct));
-        cfg.blockDim = dim3(S::kThreads);
-        cfg.dynamicSmemBytes = S::kSmem;
-        cfg.stream = st;
-        cudaLaunchAttribute at[2];
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)p.direct;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 2;
-        return cudaLaunchKernelEx(&cfg, kern, p);
+        return launch_early(kern, (unsigned)(p.B * p.Hkv * p.row_tiles * p.direct), S::kThreads, S::kSmem, st, p,
+                            (unsigned)p.direct);
     }
     using S = Shape<D, NT, false>;
     const auto kern = paged_attn_kernel<D, NT, F16, false>;

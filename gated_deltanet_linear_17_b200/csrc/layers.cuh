@@ -8,28 +8,30 @@
 namespace gdn {
 
 // ---------------------------------------------------------------- launches that overlap their predecessor's end
-// Every kernel of gdn_layers.h is launched with launch_early: its CTAs may come to lie on the SMs while the
-// kernel before it in the stream is still at work, and wait in begin_early, before their first access to memory,
-// until that one is complete and its writes visible.  A kernel that has called begin_early lets its own successor
-// in likewise (once all its CTAs run, so the successor takes no room from them).
-__device__ __forceinline__ void begin_early()
-{
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// Every kernel of gdn_layers.h is launched with launch_early: its launch is prepared while the kernel before it in
+// the stream ends, and begin_early waits, before the first access to memory, until that one is complete and its
+// writes visible.  No kernel lets its successor's CTAs in before its own have left the SMs
+// (griddepcontrol.launch_dependents), but for the paged attention its join: a grid cut to fill the GPU once finds
+// no room for its last CTAs where a few that still run have broken up an SM's shared memory, and they start only
+// when others end (37 ragged sequences 55 -> 80 us).
+__device__ __forceinline__ void begin_early() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 template <class K, class P>
-cudaError_t launch_early(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t st, const P &p)
+cudaError_t launch_early(K kernel, unsigned grid, unsigned block, size_t smem, cudaStream_t st, const P &p,
+                         unsigned cluster = 1)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
