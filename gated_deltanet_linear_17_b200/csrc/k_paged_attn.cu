@@ -39,7 +39,6 @@ namespace gdn {
 
 namespace {
 
-constexpr int kTile = 16;  // keys a warp takes at a time
 constexpr float kLn2 = 0.693147181f;
 
 // NT: octets of query rows (1 or 2).  A warp's ring of 256-column tiles takes 48 KB: two CTAs of two warps an SM
@@ -47,8 +46,10 @@ constexpr float kLn2 = 0.693147181f;
 template <int D, int NT, bool DIRECT>
 struct Shape {
     static constexpr int kWarps = D == 256 && !DIRECT ? 2 : 4, kThreads = 32 * kWarps;
-    static constexpr int kCtas = DIRECT ? kDirectCtasPerSm(D) : kAttnCtasPerSm(D);
-    static constexpr int kStages = D == 64 ? 4 : 3;
+    static constexpr int kTile = D == 64 ? 32 : 16;  // keys a warp takes at a time: 16 narrow ones are too little work
+    static constexpr int kSteps = kTile / 16;        // for what a tile costs beside them (ragged batch 58 -> XX us)
+    static constexpr int kCtas = DIRECT ? kDirectCtasPerSm(D) : kAttnCtasPerSm;
+    static constexpr int kStages = 3;
     static constexpr int kHalf = kTile * D * 2;      // bytes of a tile's keys (or values)
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kRing = kStages * kStage;   // per warp
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     paged_attn_kernel(const AttnParams p)
 {
     using S = Shape<D, NT, DIRECT>;
-    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows, kStages = S::kStages;
+    constexpr int kWarps = S::kWarps, kThreads = S::kThreads, kRows = S::kRows, kStages = S::kStages, kTile = S::kTile, kSteps = S::kSteps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
     __shared__ int wslot[kWarps];     // the stage that holds a warp's sums while the warps are joined
@@ -261,7 +262,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         cut<D>(now, p);
     }
 
-    // this warp's tiles of a piece: those at k0 + 16 (warp + kWarps i)
+    // this warp's tiles of a piece: those at k0 + kTile (warp + kWarps i)
     auto tiles_of = [&](const Piece &c) {
         const int tiles = (c.k1 - c.k0 + kTile - 1) / kTile;
         return tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     // The next tile to be looked up: the i-th of piece `ahead`, of which this warp has `count`.
     Piece ahead = now;
     int i_ahead = 0, count = tiles_of(ahead);
-    // A tile to be fetched: the cache row of its key (lane % 16), -1 behind the piece's last key, -2 on a page outside
+    // A tile to be fetched: the cache row of its key (lane % kTile), -1 behind the piece's last key, -2 on a page outside
     // the cache; and its head, or -1 when there is none left.  It is looked up a tile ahead of its use.
     struct Tile {
         int row, hkv;
@@ -283,7 +284,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         Tile t = {-1, -1};
         if (i_ahead >= count) return t;
         t.hkv = ahead.pair / p.row_tiles;
-        const int j = ahead.k0 + kTile * (warp + kWarps * i_ahead) + (lane & 15);
+        const int j = ahead.k0 + kTile * (warp + kWarps * i_ahead) + (lane & (kTile - 1));
         if (j < ahead.k1) {
             t.row = attn_cache_row(p.table + (long long)ahead.b * p.max_pages, j, p.by_page, p.page_size, p.P);
             if (t.row < 0) t.row = -2;
@@ -389,31 +390,39 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             bad |= bad_pages >> stage & 1;
             stage = stage + 1 == kStages ? 0 : stage + 1;
 
-            // scores of the query rows against 16 keys; even and odd steps apart, to halve the chain of additions
-            float s[2][4] = {}, s1[2][4] = {};
+            // scores of the query rows against the tile's keys; with 16 of them even and odd steps apart, to halve the
+            // chain of additions
+            float s[2 * kSteps][4] = {}, s1[2][4] = {};
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(ks + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b0, b1, b2, b3);
                 if (!S::kQInRegs) query(k, qf[0]);
                 const uint32_t *a = qf[S::kQInRegs ? k : 0];
-                mma<F16>(k & 1 ? s1[0] : s[0], a, b0, b1);
-                mma<F16>(k & 1 ? s1[1] : s[1], a, b2, b3);
-            }
-            const int left = now.k1 - (now.k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. 16, or more)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+                for (int h = 0; h < kSteps; ++h) {
+                    uint32_t b0, b1, b2, b3;
+                    ldsm_x4(ks + sw<D>(16 * h + (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), b0, b1,
+                            b2, b3);
+                    mma<F16>(kSteps == 1 && k & 1 ? s1[0] : s[2 * h], a, b0, b1);
+                    mma<F16>(kSteps == 1 && k & 1 ? s1[1] : s[2 * h + 1], a, b2, b3);
+                }
+            }
+            const int left = now.k1 - (now.k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. kTile, or more)
+#pragma unroll
+            for (int t = 0; t < 2 * kSteps; ++t)
 #pragma unroll
                 for (int e = 0; e < 2 * NT; ++e) {
                     const int key = 8 * t + 2 * (lane & 3) + (e & 1);
-                    s[t][e] = key < left ? (s[t][e] + s1[t][e]) * p.scale_log2 : -INFINITY;
+                    const float f = kSteps == 1 ? s[t][e] + s1[t & 1][e] : s[t][e];
+                    s[t][e] = key < left ? f * p.scale_log2 : -INFINITY;
                 }
             float alpha[NT], ref[NT];
             bool moved = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
-                const float top =
-                    quad_max(fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1])));
+                float top = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 2 * kSteps; ++t) top = fmaxf(top, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
+                top = quad_max(top);
                 const float most = fmaxf(m[r], top);
                 ref[r] = most == -INFINITY ? 0.f : most;  // every score -infinity so far: the exponentials are 0
                 alpha[r] = exp2f(m[r] - ref[r]);
@@ -437,25 +446,27 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             }
             // The scores' fragment (query row lane / 4, keys 2 (lane % 4) + ..) is, packed, the second operand of
             // V^T P^T (its column lane / 4, its rows 2 (lane % 4) + ..): no exchange between lanes.
-            uint32_t hi[NT][2], lo[NT][2];
+            uint32_t hi[NT][2 * kSteps], lo[NT][2 * kSteps];
 #pragma unroll
             for (int r = 0; r < NT; ++r)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
+                for (int t = 0; t < 2 * kSteps; ++t) {
                     const float p0 = exp2f(s[t][2 * r] - ref[r]), p1 = exp2f(s[t][2 * r + 1] - ref[r]);
                     l[r] += p0 + p1;
                     split2<F16>(p0, p1, hi[r][t], lo[r][t]);
                 }
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) {
-                uint32_t a[4];
-                ldsm_x4_t(vs + sw<D>((lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0], a[1], a[2],
-                          a[3]);
+            for (int t = 0; t < D / 16; ++t)
 #pragma unroll
-                for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][0], hi[r][1]);
+                for (int h = 0; h < kSteps; ++h) {
+                    uint32_t a[4];
+                    ldsm_x4_t(vs + sw<D>(16 * h + (lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0],
+                              a[1], a[2], a[3]);
 #pragma unroll
-                for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][0], lo[r][1]);
-            }
+                    for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][2 * h], hi[r][2 * h + 1]);
+#pragma unroll
+                    for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][2 * h], lo[r][2 * h + 1]);
+                }
         }
 
         // The end of the piece: join the warps.  A warp's sums go to its free stage; the next piece's queries are on
@@ -783,7 +794,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len)
     const int keys = D == 256 && pairs > slots ? kDirectKeysQueued : kDirectKeys;
     if (max_len <= (long long)keys * cluster && pairs < (1 << 24)) return AttnPlan{0, cluster};
     const long long most = pairs * ((max_len + kAttnUnit - 1) / kAttnUnit);
-    return AttnPlan{(int)std::min(std::max(most, 2LL), (long long)kAttnSms * kAttnCtasPerSm(D)), 0};
+    return AttnPlan{(int)std::min(std::max(most, 2LL), (long long)kAttnSms * kAttnCtasPerSm), 0};
 }
 
 template <int D, bool F16>

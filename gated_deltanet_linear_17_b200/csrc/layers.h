@@ -55,9 +55,9 @@ struct RopeParams {
 cudaError_t launch_rope(const RopeParams &p, int act_dtype, bool interleaved, cudaStream_t st);
 
 constexpr int kAttnUnit = 64, kAttnSms = 148, kAttnMaxCluster = 8;
-constexpr int kAttnCtasPerSm(int D) { return D == 64 ? 3 : 2; }
-constexpr int kDirectCtasPerSm(int D) { return D == 64 ? 3 : D == 128 ? 2 : 1; }
-constexpr int kAttnMaxCtas = kAttnSms * 3;
+constexpr int kAttnCtasPerSm = 2;
+constexpr int kDirectCtasPerSm(int D) { return D == 256 ? 1 : 2; }
+constexpr int kAttnMaxCtas = kAttnSms * kAttnCtasPerSm;
 // The paged attention's grid, by the sizes and the longest sequence that the caller expects; any is right for any
 // lengths.  direct: CTAs of the cluster that takes a pair of a sequence and a head group, or 0; then ctas fill
 // the GPU once (fewer where there is one for each kAttnUnit keys) and share all pairs evenly.
