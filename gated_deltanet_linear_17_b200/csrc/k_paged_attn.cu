@@ -4,7 +4,8 @@
 //
 // Every key and value is read once from HBM and used by the G = Hq / Hkv query heads of its head:
 // G flops a byte of a 16-bit cache, so up to G of about 250 the cache's bytes bound it, and the matrix
-// products (mma.sync: 16 query rows, zero-padded, against 8 keys or columns) only have to keep up.
+// products only have to keep up: mma.sync, which takes its operands from any shared-memory tile and leaves
+// the softmax its scores in registers; one octet of query rows costs a sixth of the SM's time.
 //
 // The split.  The work is one list of units of 64 keys, ordered by sequence, then by key/value head
 // (and group of 16 query heads), then along the keys.  The grid fills the GPU once and CTA i of C takes
@@ -13,17 +14,16 @@
 // has to be known on the host.  A part covers the end of one (sequence, head) pair, whole pairs, and
 // the beginning of another.  Whole pairs are written out; an incomplete one leaves its unnormalised sum,
 // maximum and sum of exponentials in one of the CTA's two places in the workspace, and a second kernel
-// joins a pair's pieces in their order, so the result does
-// not depend on the order in which CTAs run.
+// joins a pair's pieces in their order, so the result does not depend on the order in which CTAs run.
 //
-// Short sequences (attn_direct) do without the list, the workspace and the second kernel: each pair is one
+// Short sequences (attn_plan) do without the list, the workspace and the second kernel: each pair is one
 // cluster's, its keys cut over the cluster's CTAs, which join their results through distributed shared
 // memory.
 //
-// Inside a CTA four warps take every fourth tile of 16 keys.  A warp is on its own until the end of the
+// Inside a CTA the warps take tiles of 16 or 32 keys in turn.  A warp is on its own until the end of the
 // piece: its own ring of tiles in shared memory, filled by cp.async a few tiles ahead, its own running
 // maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end of a piece the
-// four partial results are joined through shared memory, while the next piece's tiles are on their way.
+// warps' results are joined through shared memory, while the next piece's tiles are on their way.
 //
 // Roundings.  Scores, exponentials (base 2, the scale folded in), sums and outputs are fp32.  The
 // probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
@@ -47,7 +47,8 @@ template <int D, int NT, bool DIRECT>
 struct Shape {
     static constexpr int kWarps = D == 256 && !DIRECT ? 2 : 4, kThreads = 32 * kWarps;
     static constexpr int kTile = D == 64 ? 32 : 16;  // keys a warp takes at a time: 16 narrow ones are too little work
-    static constexpr int kSteps = kTile / 16;        // for what a tile costs beside them (ragged batch 58 -> XX us)
+    static constexpr int kSteps = kTile / 16;        // for what a tile costs beside them (16 sequences of 8 heads, up
+                                                     // to 8000 keys: 39 us with 16, 36 us with 32)
     static constexpr int kCtas = DIRECT ? kDirectCtasPerSm(D) : kAttnCtasPerSm;
     static constexpr int kStages = 3;
     static constexpr int kHalf = kTile * D * 2;      // bytes of a tile's keys (or values)
@@ -777,24 +778,26 @@ cudaError_t launch(const AttnParams &p, cudaStream_t st)
 
 }  // namespace
 
-// A cluster a pair where that leaves a CTA at most kDirectKeys keys; measured (us, clusters against the list):
-//   1 sequence of 2 heads, D = 128: 512 keys 5.8 / 8.1, 2048 keys 8.1 / 9.1, 4096 keys (512 a CTA) 11.4 / 9.9
-//   1 sequence of 2 heads, D = 256: 512 keys 8.1 / 13.6, 2048 keys 12.4 / 14.1, 4096 keys 17.3 / 15.1
-//   16 sequences of 8 heads, D = 128: 512 keys (256 a CTA) 9.4 / 13.6, 2048 keys of unequal lengths 19.6 / 20.7
-//   64 sequences of 8 heads (more pairs than CTAs fit at once), D = 128: 256 keys 13 / 18, 2048 keys of unequal
-//   lengths 67 / 56; D = 256, one CTA an SM: 64 keys 15 / 19, 256 keys 40 / 37, hence kDirectKeysQueued there
-constexpr int kDirectKeys = 256, kDirectKeysQueued = 64;
-static_assert(kDirectKeys >= kAttnUnit && kDirectKeysQueued >= kAttnUnit, "a list has two units or more");
+// A cluster a pair where that leaves a CTA few keys; measured (us on the device, clusters against the list; a
+// second figure: lengths from an eighth to the whole):
+//   1 sequence of 2 heads, clusters of 8: D = 128, 1024 keys 6.7 / 8.5, 2048 keys (256 a CTA) 8.5 / 8.4, 4096 keys
+//   11.9 / 9.0; D = 256, 1024 keys 10.0 / 12.8, 2048 keys 12.7 / 13.1, 4096 keys 17.8 / 13.8
+//   4 sequences of 8 heads: D = 128, clusters of 8, 4096 keys (512 a CTA) 14.3, 13.1 / 18.1, 16.2; D = 256, clusters
+//   of 4, 2048 keys (512) 18.0, 16.7 / 22.8, 19.7
+//   64 sequences of 8 heads, more pairs than CTAs fit at once: D = 128, 512 keys 29, 20 / 33, 22, 1024 keys 49, 38 /
+//   54, 35; D = 256, one CTA an SM, 64 keys 15 / 19, 256 keys 42, 30 / 36, 27
+constexpr int kDirectKeys = 256, kDirectKeysMany = 512, kManyPairs = 16, kDirectKeysQueued = 64;
+static_assert(kDirectKeysQueued >= kAttnUnit, "a list has two units or more");
 
 AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len)
 {
     const long long pairs = (long long)B * Hkv * ((Hq / Hkv + 15) / 16), slots = kAttnSms * kDirectCtasPerSm(D);
     int cluster = 1;
     while (cluster < kAttnMaxCluster && pairs * cluster * 2 <= slots) cluster *= 2;
-    const int keys = D == 256 && pairs > slots ? kDirectKeysQueued : kDirectKeys;
+    const int keys = D == 256 && pairs > slots ? kDirectKeysQueued : pairs < kManyPairs ? kDirectKeys : kDirectKeysMany;
     if (max_len <= (long long)keys * cluster && pairs < (1 << 24)) return AttnPlan{0, cluster};
     const long long most = pairs * ((max_len + kAttnUnit - 1) / kAttnUnit);
-    return AttnPlan{(int)std::min(std::max(most, 2LL), (long long)kAttnSms * kAttnCtasPerSm), 0};
+    return AttnPlan{(int)std::min(most, (long long)kAttnSms * kAttnCtasPerSm), 0};
 }
 
 template <int D, bool F16>

@@ -382,6 +382,17 @@ class Paged:
         self.seq_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
 
 
+    def widened(self, capacity):
+        """The same sequences in a table with room for `capacity` keys each: without a hint the work is then cut as for
+        sequences of that length."""
+        wide = Paged.__new__(Paged)
+        wide.__dict__.update(self.__dict__)
+        wide.max_pages = -(-capacity // self.page)
+        wide.table = torch.full((len(self.lens), wide.max_pages), -7, dtype=torch.int32, device="cuda")
+        wide.table[:, :self.max_pages] = self.table
+        return wide
+
+
 def attn64(q, keys, values, scale):
     """(out, lse, the tolerance's sum p |v| and e) of one sequence, in 64 bits."""
     Hq, D = q.shape
@@ -434,6 +445,11 @@ def test_attn_lengths(D, dtype, page):
         check_attn(q, c, max_seqlen=hint)
     again = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, output_lse=True)
     assert torch.equal(a[0], again[0]) and torch.equal(a[1], again[1])   # run to run, bit for bit
+    wide = c.widened(100000)
+    assert gdn.paged_attn_workspace_bytes(len(lens), 6, 2, D, page, wide.max_pages) > 0
+    a = check_attn(q, wide)                                               # cut by the list
+    again = gdn.paged_attn_fwd(q, wide.k, wide.v, wide.table, wide.seq_lens, output_lse=True)
+    assert torch.equal(a[0], again[0]) and torch.equal(a[1], again[1])
 
 
 @pytest.mark.parametrize("Hkv, G", [(1, 1), (3, 2), (2, 7), (1, 8), (2, 9), (1, 16), (1, 17), (2, 24), (1, 40), (12, 1)])
@@ -441,7 +457,19 @@ def test_attn_lengths(D, dtype, page):
 def test_attn_heads(Hkv, G, D):
     lens = [700, 3, 0, 1290]
     c = Paged(lens, Hkv, D, 16, BF16, seed=G)
-    check_attn(randn(gen(2), len(lens), Hkv * G, D), c)
+    q = randn(gen(2), len(lens), Hkv * G, D)
+    check_attn(q, c)
+    check_attn(q, c.widened(100000))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attn_many_short_sequences(D):
+    """More pairs than CTAs, several of them one after the other in a CTA, empty ones among them."""
+    lens = [(7 * i * i + 3 * i) % 150 if i % 5 else 0 for i in range(260)]
+    c = Paged(lens, 3, D, 16, F16, seed=31)
+    q = randn(gen(31), len(lens), 6, D, dtype=F16)
+    check_attn(q, c)
+    check_attn(q, c.widened(20000))
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
@@ -486,6 +514,7 @@ def test_attn_scores_far_below_zero(D):
         t.copy_(-t.abs() - 2)
     for hint in (0, 2000, 64, 1 << 20):
         check_attn(q, c, scale=500.0 / D, max_seqlen=hint)
+    check_attn(q, c.widened(100000), scale=500.0 / D)
 
 
 def test_attn_infinite_scores():
@@ -519,6 +548,9 @@ def test_attn_bad_rows_are_refused_alone():
     q = randn(gen(8), len(lens), 8, 128)
     check_attn(q, c, skip=(0, 1, 2, 3, 4))
     check_attn(q, c, skip=(0, 1, 2, 3, 4), max_seqlen=64)
+    wide = c.widened(100000)
+    wide.seq_lens[2] = wide.max_pages * 16 + 1
+    check_attn(q, wide, skip=(0, 1, 2, 3, 4))
 
 
 def test_attn_no_pages():
