@@ -81,6 +81,14 @@ __device__ __forceinline__ void ldsm_x2(uint32_t addr, uint32_t &r0, uint32_t &r
     asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];\n" : "=r"(r0), "=r"(r1) : "r"(addr));
 }
 
+// 2^x to 2^-22, relative; below 2^-126 zero
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float quad_max(float x)
 {
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
@@ -270,7 +278,8 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     };
     // The next tile to be looked up: the i-th of piece `ahead`, of which this warp has `count`.
     Piece ahead = now;
-    int i_ahead = 0, count = tiles_of(ahead);
+    int i_ahead = 0, count = tiles_of(ahead), hkv_ahead = ahead.pair / p.row_tiles;
+    const int32_t *table = p.table + (long long)ahead.b * p.max_pages;
     // A tile to be fetched: the cache row of its key (lane % kTile), -1 behind the piece's last key, -2 on a page outside
     // the cache; and its head, or -1 when there is none left.  It is looked up a tile ahead of its use.
     struct Tile {
@@ -281,29 +290,39 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             next_piece<D>(ahead, p, heads);
             i_ahead = 0;
             count = tiles_of(ahead);
+            hkv_ahead = ahead.pair / p.row_tiles;
+            table = p.table + (long long)ahead.b * p.max_pages;
         }
         Tile t = {-1, -1};
         if (i_ahead >= count) return t;
-        t.hkv = ahead.pair / p.row_tiles;
+        t.hkv = hkv_ahead;
         const int j = ahead.k0 + kTile * (warp + kWarps * i_ahead) + (lane & (kTile - 1));
         if (j < ahead.k1) {
-            t.row = attn_cache_row(p.table + (long long)ahead.b * p.max_pages, j, p.by_page, p.page_size, p.P);
+            t.row = attn_cache_row(table, j, p.by_page, p.page_size, p.P);
             if (t.row < 0) t.row = -2;
         }
         ++i_ahead;
         return t;
     };
+    // Lane l copies 16-byte chunk l % kChunks of rows l / kChunks + i kLaneRows.  The row's low bits that the lane
+    // sets and those that i sets are apart, so the chunk's place (sw) is an exclusive or with a constant.
+    constexpr int kChunks = D / 8, kLaneRows = 32 / kChunks;
+    const uint32_t lane_row = lane / kChunks, lane_at = lane_row * (D * 2), lane_x = ((lane % kChunks) ^ lane_row) << 4;
+    const uint32_t row_bytes = p.Hkv * D * 2;
+    const char *lane_k = reinterpret_cast<const char *>(kc) + (lane % kChunks) * 16;
+    const char *lane_v = reinterpret_cast<const char *>(vc) + (lane % kChunks) * 16;
     uint32_t bad_pages = 0;  // a bit for each stage whose tile has one
     auto fetch = [&](int stage, const Tile &t) {
         if (t.hkv >= 0) {
-            const uint32_t dst = ring + stage * S::kStage;
+            const uint32_t dst = ring + stage * S::kStage + lane_at, head = (uint32_t)t.hkv * (D * 2);
+            const char *k = lane_k + head, *v = lane_v + head;
 #pragma unroll
-            for (int i = 0; i < kTile * (D / 8) / 32; ++i) {
-                const int id = lane + 32 * i, r = id / (D / 8), c = id % (D / 8);
-                const int rr = __shfl_sync(0xffffffffu, t.row, r);
-                const long long at = rr < 0 ? 0 : ((long long)rr * p.Hkv + t.hkv) * D + 8 * c;
-                cp_async16(dst + sw<D>(r, c), kc + at, rr >= 0);
-                cp_async16(dst + S::kHalf + sw<D>(r, c), vc + at, rr >= 0);
+            for (int i = 0; i < kTile / kLaneRows; ++i) {
+                const int rr = __shfl_sync(0xffffffffu, t.row, lane_row + i * kLaneRows);
+                const uint64_t at = (uint64_t)(uint32_t)max(rr, 0) * row_bytes;
+                const uint32_t to = dst + i * 512 + (lane_x ^ (((i * kLaneRows) & 7) << 4));
+                cp_async16(to, k + at, rr >= 0);
+                cp_async16(to + S::kHalf, v + at, rr >= 0);
             }
             const uint32_t bad = __any_sync(0xffffffffu, t.row == -2);
             bad_pages = (bad_pages & ~(1u << stage)) | bad << stage;
@@ -407,15 +426,21 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
                     mma<F16>(kSteps == 1 && k & 1 ? s1[1] : s[2 * h + 1], a, b2, b3);
                 }
             }
+            if (kSteps == 1) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2 * NT; ++e) s[t][e] += s1[t][e];
+            }
             const int left = now.k1 - (now.k0 + kTile * (warp + kWarps * i));  // keys of this tile (1 .. kTile, or more)
+            if (left < kTile) {
 #pragma unroll
-            for (int t = 0; t < 2 * kSteps; ++t)
+                for (int t = 0; t < 2 * kSteps; ++t)
 #pragma unroll
-                for (int e = 0; e < 2 * NT; ++e) {
-                    const int key = 8 * t + 2 * (lane & 3) + (e & 1);
-                    const float f = kSteps == 1 ? s[t][e] + s1[t & 1][e] : s[t][e];
-                    s[t][e] = key < left ? f * p.scale_log2 : -INFINITY;
-                }
+                    for (int e = 0; e < 2 * NT; ++e)
+                        if (8 * t + 2 * (lane & 3) + (e & 1) >= left) s[t][e] = -INFINITY;
+            }
+            // maxima of the scores as they are (the scale is positive); m and ref scaled, in base 2
             float alpha[NT], ref[NT];
             bool moved = false;
 #pragma unroll
@@ -423,10 +448,10 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
                 float top = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < 2 * kSteps; ++t) top = fmaxf(top, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
-                top = quad_max(top);
+                top = quad_max(top) * p.scale_log2;
                 const float most = fmaxf(m[r], top);
                 ref[r] = most == -INFINITY ? 0.f : most;  // every score -infinity so far: the exponentials are 0
-                alpha[r] = exp2f(m[r] - ref[r]);
+                alpha[r] = ex2(m[r] - ref[r]);
                 moved |= alpha[r] != 1.f;
                 m[r] = most;
                 l[r] *= alpha[r];
@@ -452,7 +477,8 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int r = 0; r < NT; ++r)
 #pragma unroll
                 for (int t = 0; t < 2 * kSteps; ++t) {
-                    const float p0 = exp2f(s[t][2 * r] - ref[r]), p1 = exp2f(s[t][2 * r + 1] - ref[r]);
+                    const float p0 = ex2(fmaf(s[t][2 * r], p.scale_log2, -ref[r]));
+                    const float p1 = ex2(fmaf(s[t][2 * r + 1], p.scale_log2, -ref[r]));
                     l[r] += p0 + p1;
                     split2<F16>(p0, p1, hi[r][t], lo[r][t]);
                 }
@@ -513,7 +539,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * r + 2 * (lane & 3) + e;
                 if (row >= rows) continue;
-                const float f = exp2f(wm[warp][row] - top_of(row));
+                const float f = ex2(wm[warp][row] - top_of(row));
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
                     os[swizzled(row, 16 * t + lane / 4)] = o[t][r][e] * f;
@@ -531,7 +557,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int w = 0; w < kWarps; ++w) {
                 const float4 y = *reinterpret_cast<const float4 *>(sums(w) + at);
                 x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                sum += wl[w][row] * exp2f(wm[w][row] - top);
+                sum += wl[w][row] * ex2(wm[w][row] - top);
             }
             if (whole) {
                 write_out<D, F16>(p, (long long)now.b * p.Hq + head0 + row, c, x, top, sum);
@@ -569,7 +595,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 #pragma unroll
                 for (int r = 0; r < kAttnMaxCluster; ++r) {
                     if (r >= p.direct) break;
-                    const float w = exp2f(part_ml[r].x - top);
+                    const float w = ex2(part_ml[r].x - top);
                     sum = fmaf(w, part_ml[r].y, sum);
                     x.x = fmaf(w, part_x[r].x, x.x), x.y = fmaf(w, part_x[r].y, x.y);
                     x.z = fmaf(w, part_x[r].z, x.z), x.w = fmaf(w, part_x[r].w, x.w);
@@ -684,7 +710,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         top = top == -INFINITY ? 0.f : top;
-        const float w = exp2f(ml.x - top), sum = warp_sum(w * ml.y);
+        const float w = ex2(ml.x - top), sum = warp_sum(w * ml.y);
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -723,11 +749,11 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
             }
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) now = fmaxf(now, ml[i].x);
-            const float ref = now == -INFINITY ? 0.f : now, keep = exp2f(top - ref);
+            const float ref = now == -INFINITY ? 0.f : now, keep = ex2(top - ref);
             x.x *= keep, x.y *= keep, x.z *= keep, x.w *= keep, sum *= keep;
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) {
-                const float w = exp2f(ml[i].x - ref);
+                const float w = ex2(ml[i].x - ref);
                 sum = fmaf(w, ml[i].y, sum);
                 x.x = fmaf(w, y[i].x, x.x), x.y = fmaf(w, y[i].y, x.y);
                 x.z = fmaf(w, y[i].z, x.z), x.w = fmaf(w, y[i].w, x.w);
@@ -746,7 +772,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const float4 y = part[i][tid];
-                const float w = exp2f(part_ml[i].x - top);
+                const float w = ex2(part_ml[i].x - top);
                 sum = fmaf(w, part_ml[i].y, sum);
                 x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
             }
