@@ -71,7 +71,8 @@ int gdn_rms_norm(const void *x, const void *residual, const void *gate, const vo
     if (rows < 0 || width <= 0 || !dtype_ok(act_dtype) || quant < GDN_QUANT_NONE || quant > GDN_QUANT_BLOCK)
         return GDN_ERR_BAD_SHAPE;
     if (weight_dtype != act_dtype && weight_dtype != GDN_DTYPE_FP32) return GDN_ERR_BAD_SHAPE;
-    if (width > GDN_NORM_MAX_WIDTH - (width % 8 ? 8 : 0) || rows >= (int64_t(1) << 31)) return GDN_ERR_UNSUPPORTED;
+    // (a warp's rows are numbered in 32 bits, those behind the last among them)
+    if (width > GDN_NORM_MAX_WIDTH - (width % 8 ? 8 : 0) || rows > (int64_t(1) << 31) - 32) return GDN_ERR_UNSUPPORTED;
     if (rows == 0) return GDN_OK;
     if (!x || !weight || !out || (residual && !residual_out) || (quant != GDN_QUANT_NONE && !scales))
         return GDN_ERR_NULL_ARG;

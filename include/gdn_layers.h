@@ -70,7 +70,7 @@ extern "C" {
  * comes out as zero.
  * Alignment: 16 bytes for the matrices and weight, 4 for scales.  Errors:
  * GDN_ERR_NULL_ARG, GDN_ERR_BAD_SHAPE (sizes, unknown codes), GDN_ERR_UNSUPPORTED
- * (width, rows >= 2^31), GDN_ERR_ALIGNMENT, GDN_ERR_OVERLAP (an output on an
+ * (width, rows > 2^31 - 32), GDN_ERR_ALIGNMENT, GDN_ERR_OVERLAP (an output on an
  * input or on another output, beyond the two cases above), GDN_ERR_CUDA.
  */
 int gdn_rms_norm(const void *x, const void *residual, const void *gate, const void *weight, float eps,

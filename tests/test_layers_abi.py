@@ -311,3 +311,9 @@ def test_attn_rows_stay_in_the_cache(lib):
             page = pages[j // page_size]
             assert row == (page * page_size + j % page_size if 0 <= page < P else -1)
             assert row < P * page_size
+
+
+@pytest.mark.parametrize("rows", [(1 << 31) - 1, (1 << 31) - 31])
+def test_norm_refuses_rows_whose_numbers_would_wrap(lib, rows):
+    """Eight rows of four columns share a warp; the numbers of those behind the last row have to fit too."""
+    assert _norm(lib, x=1 << 40, weight=1 << 50, out=1 << 45, rows=rows, width=1) == B.GDN_ERR_UNSUPPORTED
