@@ -822,7 +822,7 @@ AttnPlan attn_plan(int B, int Hq, int Hkv, int D, long long max_len)
     while (cluster < kAttnMaxCluster && pairs * cluster * 2 <= slots) cluster *= 2;
     const int keys = D == 256 && pairs > slots ? kDirectKeysQueued : pairs < kManyPairs ? kDirectKeys : kDirectKeysMany;
     if (max_len <= (long long)keys * cluster && pairs < (1 << 24)) return AttnPlan{0, cluster};
-    const long long most = pairs * ((max_len + kAttnUnit - 1) / kAttnUnit);
+    const long long most = pairs * std::max(1LL, (max_len + kAttnUnit - 1) / kAttnUnit);  // (a table may have no columns)
     return AttnPlan{(int)std::min(most, (long long)kAttnSms * kAttnCtasPerSm), 0};
 }
 

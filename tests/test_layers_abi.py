@@ -317,3 +317,9 @@ def test_attn_rows_stay_in_the_cache(lib):
 def test_norm_refuses_rows_whose_numbers_would_wrap(lib, rows):
     """Eight rows of four columns share a warp; the numbers of those behind the last row have to fit too."""
     assert _norm(lib, x=1 << 40, weight=1 << 50, out=1 << 45, rows=rows, width=1) == B.GDN_ERR_UNSUPPORTED
+
+
+def test_attn_workspace_of_many_sequences_without_pages(lib):
+    """More pairs than clusters are launched for, and a table without columns: still a list with CTAs."""
+    none = gdn.paged_attn_workspace_bytes(1 << 24, 1, 1, 64, 16, 0)
+    assert none > 0 and none == gdn.paged_attn_workspace_bytes(1 << 24, 1, 1, 64, 16, 4)
