@@ -213,10 +213,12 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         return make_uint4(w[0], w[1], w[2], w[3]);
     };
     auto mask = [&](int c, bool in, float2 (&v)[H]) {  // clears what is not in the row
-        if (!kShift || in) return;
+        if constexpr (kShift) {
+            if (in) return;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if ((unsigned)(c + j) >= (unsigned)width) (j & 1 ? v[j / 2].y : v[j / 2].x) = 0.f;
+            for (int j = 0; j < N; ++j)
+                if ((unsigned)(c + j) >= (unsigned)width) (j & 1 ? v[j / 2].y : v[j / 2].x) = 0.f;
+        }
     };
     auto store = [&](raw *m, int c, bool in, const float2 (&v)[H]) {
         if (!kShift || in) {
