@@ -4,7 +4,8 @@ the write into a paged cache, and the attention of one new token over that cache
 As in ``_binding``: shapes, types and devices are checked, torch supplies the device memory and the
 stream, and every step of the computation runs in the library's CUDA kernels.  A call runs on its
 tensors' device whatever the current device is, and on that device's current stream unless ``stream``
-is given; memory that a call allocates belongs to the stream that it runs on.
+is given; memory that a call allocates belongs to the stream that it runs on.  The operators are forward
+only: no gradient is recorded through them.
 """
 from __future__ import annotations
 
@@ -252,7 +253,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     q [B, Hq, D] bf16 or fp16, D 64, 128 or 256; k_cache, v_cache [P, page_size, Hkv, D] of q's type, Hq a
     multiple of Hkv (query head h reads key/value head h // (Hq // Hkv)); block_table [B, max_pages]
     int32, the pages of each sequence in order (entries past its last page are not read); seq_lens [B]
-    int32, the keys of each sequence, the new token's own among them.  ``max_seqlen`` is the longest
+    int32, the keys of each sequence, the new token's own among them.  ``scale`` is positive (default
+    1/sqrt(D)).  ``max_seqlen`` is the longest
     length if known, else 0 (it sets how the work is split).  A length of 0 gives a zero row and lse
     -inf; a length beyond the table or a page outside the cache gives NaN for that sequence.
     ``lse`` [B, Hq] fp32 is written when given or when ``output_lse``.  ``workspace``: a device buffer
@@ -277,6 +279,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     max_seqlen = min(int(max_seqlen), 0x7fffffff)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
+    if scale is not None and not 0.0 < scale < math.inf:
+        raise ValueError(f"scale must be positive and finite (got {scale})")
     max_pages = block_table.shape[1]
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")

@@ -142,11 +142,12 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  *                 GPU (two captured graphs among them) need workspaces of their own
  * A sequence with a length outside its range or a page outside [0, P) among its
  * pages reads nothing out of bounds and comes out as NaN (out and lse), the
- * others are not affected.
+ * others are not affected.  NaN and infinities in a sequence's own rows come out
+ * as NaN where the formula gives NaN, an infinity in v as an infinity or NaN (p is
+ * multiplied in two parts, the second of either sign); cache rows that no sequence lists are never read.
  * Alignment: 16 bytes for q, the caches, out and workspace, 4 for the rest.  Errors:
  * GDN_ERR_NULL_ARG, GDN_ERR_BAD_SHAPE, GDN_ERR_UNSUPPORTED (act_dtype, D, P *
- * page_size >= 2^31, max_pages * page_size >= 2^31, more than 65535 rows of
- * key/value heads and head groups), GDN_ERR_ALIGNMENT,
+ * page_size >= 2^31, max_pages * page_size > 2^30, B >= 2^30, Hq > 65535), GDN_ERR_ALIGNMENT,
  * GDN_ERR_WORKSPACE, GDN_ERR_OVERLAP, GDN_ERR_CUDA.  B == 0 is a no-op.
  */
 size_t gdn_paged_attn_workspace_bytes(int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,

@@ -772,3 +772,109 @@ def test_attn_allocates_its_own_workspace_in_the_library():
         None, 2, 8, 2, 128, c.k.shape[0], 16, c.max_pages, 0, 1, None, 0, torch.cuda.current_stream().cuda_stream)
     torch.cuda.synchronize()
     assert rc == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.5, NAN, float("inf")])
+def test_attn_refuses_scales_that_are_not_positive(scale):
+    """A scale at or below zero is the library's sign for its default; the binding lets none through as a value."""
+    c = Paged([30, 40], 2, 64, 16, BF16)
+    with pytest.raises(ValueError, match="scale"):
+        gdn.paged_attn_fwd(randn(gen(18), 2, 4, 64), c.k, c.v, c.table, c.seq_lens, scale=scale)
+
+
+@pytest.mark.parametrize("columns", [None, 4000])
+def test_attn_nan_and_infinite_rows_stay_with_their_sequence(columns):
+    """NaN in one sequence's keys or values, and an infinite value: that sequence alone is NaN (of the value, its
+    column alone infinite or NaN), the next in the same list as if nothing were there."""
+    c = Paged([130, 300, 1, 77], 2, 128, 16, BF16, seed=5)
+    if columns:
+        c = c.widened(columns)
+    q = randn(gen(19), 4, 8, 128)
+    want, want_lse = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, output_lse=True)
+    place = lambda b, j: (int(c.table[b, j // 16]), j % 16)
+    c.k[(*place(1, 200), 0)] = NAN              # head 0 of sequence 1
+    c.v[(*place(0, 129), 1, 7)] = float("inf")  # column 7 of head 1 of sequence 0
+    got, lse = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, output_lse=True)
+    assert got[1, :4].isnan().all() and lse[1, :4].isnan().all()
+    assert not got[0, 4:, 7].isfinite().any()   # the weight's second part may be below zero: infinity less infinity
+    keep = torch.ones_like(got, dtype=torch.bool)
+    keep[1, :4] = False
+    keep[0, 4:, 7] = False
+    assert torch.equal(got[keep], want[keep])
+    lse[1, :4] = want_lse[1, :4]
+    assert torch.equal(lse, want_lse)
+
+
+def test_attn_one_workspace_for_calls_in_order():
+    """Calls of different sizes behind one another on a stream may share a workspace, captured ones too."""
+    cs = [Paged([9000, 5], 2, 128, 16, BF16, seed=6), Paged([700] * 40, 1, 64, 16, BF16, seed=7),
+          Paged([3, 20000], 1, 256, 16, BF16, seed=8)]
+    qs = [randn(gen(20), 2, 8, 128), randn(gen(21), 40, 24, 64), randn(gen(22), 2, 8, 256)]
+    want = [gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens)[0] for q, c in zip(qs, cs)]
+    ws = torch.empty(max(gdn.paged_attn_workspace_bytes(*q.shape[:2], c.k.shape[2], q.shape[2], 16, c.table.shape[1])
+                         for q, c in zip(qs, cs)), dtype=torch.uint8, device="cuda")
+    outs = [[torch.empty_like(q) for q in qs] for _ in range(4)]
+
+    def run():
+        for out in outs:
+            for o, q, c in zip(out, qs, cs):
+                gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, out=o, workspace=ws)
+
+    run()
+    assert all(torch.equal(o, w) for out in outs for o, w in zip(out, want))
+    for out in outs:
+        for o in out:
+            o.zero_()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        run()
+    gr.replay()
+    assert all(torch.equal(o, w) for out in outs for o, w in zip(out, want))
+
+
+def test_layers_captured_with_copies_and_branches():
+    """Launches that overlap their predecessor's end, in a graph whose predecessors are copies, fills and another
+    branch's kernels: every one still waits for what it reads."""
+    g = gen(23)
+    B, Hq, Hkv, page, rows = 4, 8, 2, 16, 4096
+    c = Paged([2500, 17, 900, 16], Hkv, 128, page, BF16, seed=9)
+    f, _ = gdn.rope_inv_freq(128)
+    lens = c.seq_lens
+    pos = lens - 1
+    slots = (c.table[torch.arange(B, device="cuda"), (pos // page).long()] * page + pos % page).to(torch.int32)
+    w = randn(g, 1000)
+    new = dict(x=randn(g, rows, 1000), q=randn(g, B, Hq, 128), k=randn(g, B, Hkv, 128), v=randn(g, B, Hkv, 128))
+    held = {n: torch.zeros_like(t) for n, t in new.items()}
+    side = torch.cuda.Stream()
+
+    def step():
+        for n in new:
+            held[n].copy_(new[n])
+        side.wait_stream(torch.cuda.current_stream())
+        h, _, sc = gdn.rms_norm(held["x"], w, quant="row")
+        with torch.cuda.stream(side):
+            q, _ = gdn.rope_fwd(held["q"], held["k"], pos, f, v=held["v"], k_cache=c.k, v_cache=c.v, slots=slots)
+            o, _ = gdn.paged_attn_fwd(q, c.k, c.v, c.table, lens)
+            held["q"].zero_()
+        held["x"].zero_()                              # behind the norm that read it
+        h2, _, _ = gdn.rms_norm(held["x"], w)
+        torch.cuda.current_stream().wait_stream(side)
+        o2, _, _ = gdn.rms_norm(o, w[:128].contiguous())
+        return h, sc, q, o, h2, o2
+
+    step()
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        got = step()
+    for trial in range(3):
+        for n in new:
+            new[n].copy_(randn(g, *new[n].shape))
+        gr.replay()
+        torch.cuda.synchronize()
+        got_now = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        for a, b in zip(got_now, want):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert not want[4].any() and torch.isfinite(want[3].float()).all()
