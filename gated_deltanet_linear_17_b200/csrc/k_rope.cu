@@ -19,6 +19,10 @@
 // (interleaved), in the lane n / 8 away (shuffles), or, when n is no multiple of 8, across two lanes (read
 // again, from L1).  A warp takes as many tokens as it has room for rows, and reads up to four heads ahead of its
 // work on them; where there are few tokens, several warps share their heads.
+//
+// Measured (bf16, 32768 tokens of 16 + 2 heads of 256 with the cache's write): 108 us, 6.2 TB/s, 96 % of the copy
+// rate; with the factors read from shared memory for every head 198 us.  4099 tokens of 32 + 8 heads of 128, pairs,
+// fp16: 16.7 us, 5.0 TB/s, a third of it the kernel's start and end.  64 tokens: 2.8 us.
 #include <algorithm>
 
 #include "gdn_layers.h"
