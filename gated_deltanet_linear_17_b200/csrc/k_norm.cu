@@ -116,42 +116,44 @@ __device__ __forceinline__ float weight_at(const NormParams &p, int c, bool f16)
 
 constexpr int kNarrowBlock = 128;  // threads of a CTA whose warps hold whole rows
 __host__ __device__ constexpr int norm_block(int L) { return L <= 32 ? kNarrowBlock : L; }
-// Columns a thread holds.  32 of a 16-bit type; 16 of fp32, whose elements have twice the time and take twice the
-// ring (1537 columns with residual and gate: 39 us with 32, 8 warps an SM).
-template <class A>
-__host__ __device__ constexpr int norm_per(int L) { return sizeof(typename A::raw) == 4 && L <= 512 ? 16 : 32; }
 // CTAs an SM that the registers leave room for
-__host__ __device__ constexpr int norm_ctas(int L) { return L <= 256 ? 768 / norm_block(L) : 1024 / L; }
-// Rows up to 8192 columns come through two stages in shared memory: cp.async brings a group's next row while it
-// works on this one.  A thread fetches what it will use itself, so no barrier orders the stages.  Wider rows go
-// straight to registers.
+__host__ __device__ constexpr int norm_ctas(int L) { return L <= 384 ? 768 / norm_block(L) : 1024 / L; }
+// Rows come through shared memory: cp.async brings a group's next row while it works on this one.  A thread
+// fetches what it will use itself, so no barrier orders it, and one stage will do: the next row's x and residual
+// are asked for as soon as this one's sum is in registers, its gate after this one's use.  A second stage, with the next
+// row on its way before this one is waited for, is taken where it costs no CTA its room and a row is more than a warp's
+// (16384 x 4096 bf16 with a residual and row scales 76 us, 86 with one stage; with a gate too, where it costs two CTAs of
+// six, 105 against 94; heads of 128 with a gate 68.5 against 62); rows that begin inside a block have too many
+// instructions to gain by it (fp16, 1537 columns with a residual: 146 against 129).  fp32 rows beyond 16384 columns,
+// too wide for three of them to lie there, go straight to registers.
 template <class A>
-__host__ __device__ constexpr bool norm_ring(int L) { return L * norm_per<A>(L) <= 8192; }
+__host__ __device__ constexpr bool norm_ring(int L, int PER) { return L * PER * (int)sizeof(typename A::raw) <= 65536; }
+__host__ __device__ constexpr bool norm_two_stages(Kind kind, int L) { return kind != kShifted && L > 32; }
 // Where warps hold whole rows, the weights lie in shared memory in fp32, offset added: in order, or
 // (kShifted) as 2 N - 1 lines, line r of the weights r - (N - 1) behind the first of each unit, zeros outside the
 // row.  A unit of a row that begins ph elements into a block then reads N lines from N - 1 - ph on, its
 // neighbours beside it.
 __host__ __device__ constexpr bool norm_weights(int L) { return L <= 32; }
 template <class A>
-__host__ __device__ constexpr int norm_line(int L) { return L * norm_per<A>(L) / Unit<A>::N + 1; }
+__host__ __device__ constexpr int norm_line(int L, int PER) { return L * PER / Unit<A>::N + 1; }
 template <class A>
-__host__ __device__ constexpr int norm_weight_bytes(Kind kind, int L)
+__host__ __device__ constexpr int norm_weight_bytes(Kind kind, int L, int PER)
 {
     return !norm_weights(L)   ? 0
-           : kind != kShifted ? L * norm_per<A>(L) * 4
-                              : ((2 * Unit<A>::N - 1) * norm_line<A>(L) * 4 + 15) / 16 * 16;
+           : kind != kShifted ? L * PER * 4
+                              : ((2 * Unit<A>::N - 1) * norm_line<A>(L, PER) * 4 + 15) / 16 * 16;
 }
 __host__ __device__ constexpr int pow2(int n) { return n <= 1 ? 1 : 2 * pow2((n + 1) / 2); }
 
-// A group of L threads strides over the rows.
-template <class A, Kind KIND, int L>
+// A group of L threads of PER columns each strides over the rows.
+template <class A, Kind KIND, int L, int PER>
 __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(const NormParams p)
 {
     using U = Unit<A>;
     using raw = typename A::raw;
-    constexpr bool kRing = norm_ring<A>(L), kShared = norm_weights(L), kShift = KIND == kShifted;
+    constexpr bool kRing = norm_ring<A>(L, PER), kShared = norm_weights(L), kShift = KIND == kShifted;
     constexpr bool kF16 = std::is_same<A, F16>::value;
-    constexpr int N = U::N, H = N / 2, PER = norm_per<A>(L), NV = PER / N;
+    constexpr int N = U::N, H = N / 2, NV = PER / N;
     constexpr int W = L < 32 ? L : 32, kWarps = pow2(L / 32);  // warps, rounded up for the shuffles
     constexpr int kBlock = norm_block(L), kRows = L <= 32 ? kBlock / L : 1, kStep = L * N;
     constexpr int kGroupLanes = 128 / N;  // lanes that hold a group of 128 columns
@@ -176,32 +178,34 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     auto phase = [&](int row) { return kShift ? (int)((long long)row * width) & (N - 1) : 0; };
 
     float *weights = reinterpret_cast<float *>(smem);
-    uint8_t *ring = smem + norm_weight_bytes<A>(KIND, L);
-    constexpr int kLine = norm_line<A>(L);
-    // this thread's 16 bytes of (stage, matrix, unit); matrices in the order x, residual, gate
+    uint8_t *ring = smem + norm_weight_bytes<A>(KIND, L, PER);
+    constexpr int kLine = norm_line<A>(L, PER);
+    // this thread's 16 bytes of (matrix, unit); matrices in the order x, residual, gate
     constexpr int kPlane = kBlock * 16, kMatrix = NV * kPlane;
-    const int gate_at = residual ? 2 * kMatrix : kMatrix, stage_bytes = kMatrix * (1 + residual + gated);
-    uint8_t *mine = ring + threadIdx.x * 16;
+    const int gate_at = residual ? 2 * kMatrix : kMatrix;
+    const bool two = norm_two_stages(KIND, L) && p.two_stages;
+    const int stage_bytes = two ? kMatrix * (1 + residual + gated) : 0;
+    const uint8_t *mine = ring + threadIdx.x * 16;
     const uint32_t mine_addr = smem_addr(mine);
     // elements of the matrix from the row's first on (a block of its last rows may end behind them), as an int
     auto rest_of = [&](int row) { return (int)min(end - (long long)row * width, 1LL << 20); };
-    auto fetch = [&](int stage, int row) {
+    // a row's x and residual, or its gate, to a stage
+    auto fetch = [&](int stage, int row, bool sum, bool gates) {
         if (row < rows) {
+            const uint32_t to = mine_addr + stage * stage_bytes;
             const int c0 = v0 - phase(row), rest = kShift ? rest_of(row) : 0;
             const long long at = (long long)row * width + c0;
             const raw *fx = x + at, *fr = res + at, *fg = gate + at;
-            const uint32_t dst = mine_addr + stage * stage_bytes;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int c = c0 + k * kStep;
                 if (KIND != kFull && c >= width) continue;
                 const int bytes = !kShift ? 16 : min(16, (rest - c) * (int)sizeof(raw));
-                cp_async16_part(dst + k * kPlane, fx + k * kStep, bytes);
-                if (residual) cp_async16_part(dst + kMatrix + k * kPlane, fr + k * kStep, bytes);
-                if (gated) cp_async16_part(dst + gate_at + k * kPlane, fg + k * kStep, bytes);
+                if (sum) cp_async16_part(to + k * kPlane, fx + k * kStep, bytes);
+                if (sum && residual) cp_async16_part(to + kMatrix + k * kPlane, fr + k * kStep, bytes);
+                if (gates && gated) cp_async16_part(to + gate_at + k * kPlane, fg + k * kStep, bytes);
             }
         }
-        cp_async_commit();
     };
     // Units from here on: m points at the unit's first element, c is its column, `in` whether the whole unit lies
     // in the row.
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     // nothing and writes nothing
     const int warp_first = first - (L < 32 ? ((int)threadIdx.x & 31) / L : 0);
     const int turns = warp_first >= rows ? 0 : (rows - 1 - warp_first) / stride + 1;
-    if (kRing) fetch(0, first);
+    if (kRing) fetch(0, first, true, true);
     if (kShared) {
         if (!kShift) {
             for (int c = threadIdx.x; c < width; c += kBlock) weights[c] = weight_at(p, c, kF16) + p.weight_offset;
@@ -317,10 +321,17 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         const int ph = phase(row), c0 = v0 - ph, rest = kShift ? rest_of(row) : 0;
         const long long at = (long long)row * width + c0;
         const raw *rx = x + at, *rr = res + at, *rg = gate + at;
+        const int next = row < rows - stride ? row + stride : rows;
         const uint8_t *held = mine + (turn & 1) * stage_bytes;
         if (kRing) {
-            fetch((turn + 1) & 1, row < rows - stride ? row + stride : rows);
-            cp_async_wait<1>();
+            cp_async_commit();
+            if (two) {
+                fetch((turn + 1) & 1, next, true, true);
+                cp_async_commit();
+                cp_async_wait<1>();
+            } else {
+                cp_async_wait<0>();
+            }
         }
         auto has = [&](int k) {
             return live && (KIND == kFull || c0 + k * kStep < width);
@@ -360,6 +371,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 for (int j = 0; j < H; ++j) sum2 = ffma2(z[k][j], z[k][j], sum2);
             }
         }
+        if (kRing && !two) fetch(0, next, true, false);
         float sum = lanes_sum<W>(sum2.x + sum2.y);
         if (L > 32) {
             if ((t & 31) == 0) red[0][t >> 5] = sum;
@@ -414,6 +426,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             }
             most = absmax_nan(absmax_nan(most, m), lead);
         }
+        if (kRing && gated && !two) fetch(0, next, false, true);
         if (kShift && quant == GDN_QUANT_BLOCK) {
             if (L > 32) __syncthreads();
             else __syncwarp();
@@ -457,48 +470,58 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     }
 }
 
-template <class A, Kind KIND, int L>
+template <class A, Kind KIND, int L, int PER>
 cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
 {
-    const auto kern = rms_norm_kernel<A, KIND, L>;
+    NormParams q = p;
+    const auto kern = rms_norm_kernel<A, KIND, L, PER>;
     constexpr int block = norm_block(L), rows = L <= 32 ? block / L : 1;
     const int matrices = 1 + (p.residual != nullptr) + (p.gate != nullptr);
-    const size_t smem = norm_weight_bytes<A>(KIND, L) +
-                        (norm_ring<A>(L) ? (size_t)2 * block * norm_per<A>(L) * sizeof(typename A::raw) * matrices : 0);
+    const size_t beside = 1280 + (KIND == kShifted ? block * PER / 16 : 0);  // the static part, and the driver's KB
+    const size_t stage = norm_ring<A>(L, PER) ? (size_t)block * PER * sizeof(typename A::raw) * matrices : 0;
+    size_t smem = norm_weight_bytes<A>(KIND, L, PER) + stage;
+    q.two_stages = norm_two_stages(KIND, L) && (int)(kNormSmem / (smem + stage + beside)) >= norm_ctas(L);
+    if (q.two_stages) smem += stage;
     if (smem > 47 * 1024) {  // 48 KB with the static part
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
-    const int per_sm = std::max(1, std::min(norm_ctas(L), (int)(kNormSmem / (smem + 1280))));
+    const int per_sm = std::max(1, std::min(norm_ctas(L), (int)(kNormSmem / (smem + beside))));
     const long long want = (p.rows + rows - 1) / rows;
-    return launch_early(kern, (unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem, st, p);
+    return launch_early(kern, (unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem, st, q);
 }
 
-// The threads of a row: the fewest of those built that hold `places` places, at least `least`.
+// The threads of a row: the fewest of those built that hold `places` places, at least `least`.  A thread holds 32
+// columns of a 16-bit type; 16 of fp32, whose elements have twice the time and take twice the room (1537 columns
+// with residual and gate: 39 us with 32, 8 warps an SM), until a CTA has no more threads.
 template <class A, Kind KIND, int L, int... MORE>
 cudaError_t launch_lanes(const NormParams &p, int places, int least, cudaStream_t st)
 {
-    if constexpr (sizeof...(MORE) > 0)
-        if (L < least || L * norm_per<A>(L) < places) return launch_lanes<A, KIND, MORE...>(p, places, least, st);
-    return launch_kernel<A, KIND, L>(p, st);
+    constexpr int PER = sizeof(typename A::raw) == 4 ? 16 : 32;
+    if constexpr (sizeof...(MORE) > 0) {
+        if (L < least || L * PER < places) return launch_lanes<A, KIND, MORE...>(p, places, least, st);
+    } else if constexpr (PER == 16) {
+        if (L * PER < places) return launch_kernel<A, KIND, L, 32>(p, st);
+    }
+    return launch_kernel<A, KIND, L, PER>(p, st);
 }
 
 template <class A>
 cudaError_t launch_type(NormParams p, cudaStream_t st)
 {
-    constexpr int N = Unit<A>::N;
+    constexpr int N = Unit<A>::N, PER = sizeof(typename A::raw) == 4 ? 16 : 32;
     const int width = p.width;
     if (p.quant == GDN_QUANT_BLOCK && width <= GDN_QUANT_GROUP) p.quant = GDN_QUANT_ROW;  // one group a row
     const int least = p.quant == GDN_QUANT_BLOCK ? 128 / N : 0;  // lanes that hold a group
     if (width % N == 0) {
         int lanes = std::max(4, least);
-        while (lanes * norm_per<A>(lanes) < width) lanes *= 2;
-        return lanes * norm_per<A>(lanes) == width
+        while (lanes < 1024 && lanes * PER < width) lanes *= 2;
+        return lanes * PER == width || 1024 * 32 == width
                    ? launch_lanes<A, kFull, 4, 8, 16, 32, 64, 128, 256, 512, 1024>(p, width, least, st)
-                   : launch_lanes<A, kAligned, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 320, 384, 512, 1024>(p, width, least, st);
+                   : launch_lanes<A, kAligned, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 320, 384, 448, 512, 640, 768, 1024>(p, width, least, st);
     }
     // a row that begins inside a block takes up to a unit more
-    return launch_lanes<A, kShifted, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 512, 1024>(p, width + N - 1, least, st);
+    return launch_lanes<A, kShifted, 4, 8, 16, 32, 64, 96, 128, 160, 192, 256, 320, 384, 512, 768, 1024>(p, width + N - 1, least, st);
 }
 
 }  // namespace

@@ -39,6 +39,7 @@ struct NormParams {
     int width;
     int quant;        // GDN_QUANT_*
     bool weight_f32;
+    bool two_stages;  // of a row in shared memory (set by the launcher)
 };
 cudaError_t launch_rms_norm(const NormParams &p, int act_dtype, cudaStream_t st);
 
