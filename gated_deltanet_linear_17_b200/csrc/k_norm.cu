@@ -20,8 +20,8 @@
 // shared memory.
 //
 // Measured: 16384 x 4096 bf16 with a residual and row scales 76 us, 6.1 TB/s, 95 % of the copy rate; 1048576 heads
-// of 128 with a gate and 8 bits 115 us, 5.9 TB/s; 4099 x 1537 fp32 with residual and gate (kShifted) 31 us, 4.1 TB/s;
-// 8 x 2048 2.4 us.
+// of 128 with a gate and 8 bits 110 us, 6.1 TB/s; 4099 x 1537 fp32 with residual and gate (kShifted) 27 us, 4.6 TB/s;
+// 8 x 2048 2.5 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -129,19 +129,26 @@ __host__ __device__ constexpr int norm_ctas(int L) { return L <= 384 ? 768 / nor
 template <class A>
 __host__ __device__ constexpr bool norm_ring(int L, int PER) { return L * PER * (int)sizeof(typename A::raw) <= 65536; }
 __host__ __device__ constexpr bool norm_two_stages(Kind kind, int L) { return kind != kShifted && L > 32; }
-// Where warps hold whole rows, the weights lie in shared memory in fp32, offset added: in order, or
-// (kShifted) as 2 N - 1 lines, line r of the weights r - (N - 1) behind the first of each unit, zeros outside the
-// row.  A unit of a row that begins ph elements into a block then reads N lines from N - 1 - ph on, its
-// neighbours beside it.
-__host__ __device__ constexpr bool norm_weights(int L) { return L <= 32; }
+// Where warps hold whole rows, and in kShifted, the weights lie in shared memory in fp32, offset added; else they come
+// from L1 in 16-byte blocks.  In order, or in kShifted in lines along which a unit's neighbours lie beside it, with zeros
+// outside the row.  L <= 32: 2 N - 1 lines, line r holds at i the weight N i + r - (N - 1); a unit i of a row that begins
+// ph elements into a block reads lines N - 1 - ph to 2 N - 2 - ph at i, all at one distance.  L > 32, for half the
+// room: N lines, line r holds the weight N i + r at i + 1; a unit's element j lies in line (j - ph) mod N, at i + 1, or
+// at i where j < ph.  (With a weight at a time from L1: 16384 x 4097 bf16 with a residual 120 us, so 90.)  Up to 10240
+// places of 16 bits, 12288 of fp32: beyond, they take a CTA's room (12001 columns bf16 with a residual 98 us against
+// 110, but with a gate too 182 against 139).
 template <class A>
 __host__ __device__ constexpr int norm_line(int L, int PER) { return L * PER / Unit<A>::N + 1; }
+__host__ __device__ constexpr bool norm_weights(Kind kind, int L, int PER)
+{
+    return L <= 32 || (kind == kShifted && L * PER <= (PER == 16 ? 12288 : 10240));
+}
 template <class A>
 __host__ __device__ constexpr int norm_weight_bytes(Kind kind, int L, int PER)
 {
-    return !norm_weights(L)   ? 0
-           : kind != kShifted ? L * PER * 4
-                              : ((2 * Unit<A>::N - 1) * norm_line<A>(L, PER) * 4 + 15) / 16 * 16;
+    return !norm_weights(kind, L, PER) ? 0
+           : kind != kShifted          ? L * PER * 4
+                                       : ((L <= 32 ? 2 * Unit<A>::N - 1 : Unit<A>::N) * norm_line<A>(L, PER) * 4 + 15) / 16 * 16;
 }
 __host__ __device__ constexpr int pow2(int n) { return n <= 1 ? 1 : 2 * pow2((n + 1) / 2); }
 
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
 {
     using U = Unit<A>;
     using raw = typename A::raw;
-    constexpr bool kRing = norm_ring<A>(L, PER), kShared = norm_weights(L), kShift = KIND == kShifted;
+    constexpr bool kRing = norm_ring<A>(L, PER), kShared = norm_weights(KIND, L, PER), kShift = KIND == kShifted;
     constexpr bool kF16 = std::is_same<A, F16>::value;
     constexpr int N = U::N, H = N / 2, NV = PER / N;
     constexpr int W = L < 32 ? L : 32, kWarps = pow2(L / 32);  // warps, rounded up for the shuffles
@@ -246,7 +253,8 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 if ((unsigned)(c + j) < (unsigned)width) m[j] = to_e4m3(j & 1 ? v[j / 2].y : v[j / 2].x);
         }
     };
-    auto weigh = [&](int k, int c, int ph, bool in, float2 (&w)[H]) {  // the weights of unit k
+    int lines[kShared && kShift && L > 32 ? N : 1];  // places of the weights of this row's first unit here
+    auto weigh = [&](int k, int c, bool in, float2 (&w)[H]) {  // the weights of unit k
         if constexpr (kShared && !kShift) {
 #pragma unroll
             for (int i = 0; i < N / 4; ++i) {
@@ -256,9 +264,8 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             }
             return;
         } else if constexpr (kShared) {
-            const float *line = weights + (N - 1 - ph) * kLine + t + k * L;
 #pragma unroll
-            for (int j = 0; j < H; ++j) w[j] = make_float2(line[2 * j * kLine], line[(2 * j + 1) * kLine]);
+            for (int j = 0; j < N; ++j) (j & 1 ? w[j / 2].y : w[j / 2].x) = weights[L <= 32 ? lines[0] + j * kLine + k * L : lines[j] + k * L];
             return;
         }
         if (!kShift || in) {
@@ -302,10 +309,13 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         if (!kShift) {
             for (int c = threadIdx.x; c < width; c += kBlock) weights[c] = weight_at(p, c, kF16) + p.weight_offset;
         } else {
-            for (int i = threadIdx.x; i < (2 * N - 1) * kLine; i += kBlock) {
+            for (int i = threadIdx.x; L <= 32 && i < (2 * N - 1) * kLine; i += kBlock) {
                 const int line = i / kLine, c = (i - line * kLine) * N + line - (N - 1);
                 weights[i] = c >= 0 && c < width ? weight_at(p, c, kF16) + p.weight_offset : 0.f;
             }
+            if (L > 32 && threadIdx.x < N) weights[threadIdx.x * kLine] = 0.f;
+            for (int c = threadIdx.x; L > 32 && c < L * PER; c += kBlock)
+                weights[c % N * kLine + c / N + 1] = c < width ? weight_at(p, c, kF16) + p.weight_offset : 0.f;
         }
     }
     if (kShift) {
@@ -380,6 +390,11 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         }
         const float rstd = rsqrtf(fmaf(sum, p.inv_width, p.eps));
 
+        if constexpr (kShared && kShift) {
+#pragma unroll
+            for (int j = 0; j < (L <= 32 ? 1 : N); ++j)
+                lines[j] = L <= 32 ? (N - 1 - ph) * kLine + t : ((j - ph) & (N - 1)) * kLine + t + (j >= ph);
+        }
         const bool leads = (t & (kGroupLanes - 1)) == 0;  // whether this thread's units begin groups
         float most = 0.f;
 #pragma unroll
@@ -390,7 +405,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
             float m = 0.f, lead = 0.f;
             if (has(k)) {
                 float2 w[H];
-                weigh(k, c, ph, in, w);
+                weigh(k, c, in, w);
 #pragma unroll
                 for (int j = 0; j < H; ++j) z[k][j] = fmul2(fmul2(z[k][j], make_float2(rstd, rstd)), w[j]);
                 if (gated) {
@@ -401,13 +416,16 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                     for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], silu(g[j]));
                 }
                 if (quant == GDN_QUANT_NONE) store(static_cast<raw *>(p.out) + at + k * kStep, c, in, z[k]);
-                else {
+                else if (kShift && quant == GDN_QUANT_BLOCK) {
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
                         const float f = j & 1 ? z[k][j / 2].y : z[k][j / 2].x;
-                        if (kShift && leads && j < ph) lead = absmax_nan(lead, f);
+                        if (leads && j < ph) lead = absmax_nan(lead, f);
                         else m = absmax_nan(m, f);
                     }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < H; ++j) m = absmax_nan(absmax_nan(m, z[k][j].x), z[k][j].y);
                 }
             }
             if (quant == GDN_QUANT_BLOCK) {
