@@ -50,10 +50,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_Tensor, _f32, _i32 = torch.Tensor, torch.float32, torch.int32
+
+
 def _need(t, name, dtype, shape, index):
     """``_binding._need`` (on CUDA device ``index``), with the comparisons of a good tensor kept cheap: a decode step's
     calls take a few microseconds."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == index
             and t.is_contiguous()):
         _b._need(t, name, dtype, shape, torch.device("cuda", index))
 
@@ -71,11 +74,15 @@ def _on(index, stream):
 _current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
 
+def _tensor(t, name):
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
+
+
 def _cuda(t, name):
     """The index of the CUDA device that t lies on."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    index = t.get_device()
+    index = _tensor(t, name).get_device()
     if index < 0 or not t.is_cuda:
         raise RuntimeError(f"{name} must be on a CUDA device (got {t.device})")
     return index
@@ -111,8 +118,7 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
     width = shape[-1]
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _cuda(weight, "weight")
-    wdt = torch.float32 if weight.dtype == torch.float32 else act
+    wdt = _f32 if _tensor(weight, "weight").dtype is _f32 else act
     _need(weight, "weight", wdt, (width,), dev)
     if residual is not None:
         _need(residual, "residual", act, shape, dev)
@@ -130,17 +136,18 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
     if scales is not None:
         if quant is None:
             raise ValueError("scales need quant")
-        _need(scales, "scales", torch.float32, sshape, dev)
+        _need(scales, "scales", _f32, sshape, dev)
     if out is None:
         out = torch.empty_like(x) if quant is None else torch.empty_like(x, dtype=odt)
     if residual is not None and residual_out is None:
         residual_out = torch.empty_like(x)
     if quant is not None and scales is None:
-        scales = x.new_empty(sshape, dtype=torch.float32)
-    rc = _layers_lib().gdn_rms_norm(_ptr(x), _ptr(residual), _ptr(gate), _ptr(weight), eps, weight_offset, _ptr(out),
-                                    _ptr(residual_out), _ptr(scales), x.numel() // width, width, _b.DTYPES[act],
-                                    _b.DTYPES[wdt], QUANT[quant], _current_stream(dev))
-    _b._check(rc, "gdn_rms_norm")
+        scales = x.new_empty(sshape, dtype=_f32)
+    rc = _layers_lib().gdn_rms_norm(x.data_ptr(), _ptr(residual), _ptr(gate), weight.data_ptr(), eps, weight_offset,
+                                    out.data_ptr(), _ptr(residual_out), _ptr(scales), x.numel() // width, width,
+                                    _b.DTYPES[act], _b.DTYPES[wdt], QUANT[quant], _current_stream(dev))
+    if rc:
+        _b._check(rc, "gdn_rms_norm")
     return out, residual_out, scales
 
 
@@ -195,8 +202,7 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     if stream is not None or dev != _current_device():
         with _on(dev, stream):
             return rope_fwd(q, k, positions, inv_freq, v, k_cache, v_cache, slots, interleaved, mscale, q_out, k_out)
-    _cuda(k, "k")
-    if q.dim() != 3 or k.dim() != 3:
+    if q.dim() != 3 or _tensor(k, "k").dim() != 3:
         raise ValueError("q must be [T, Hq, D] and k [T, Hkv, D]")
     act = _act(q, "q")
     T, Hq, D = q.shape
@@ -204,24 +210,24 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _need(k, "k", act, (T, Hkv, D), dev)
-    _need(positions, "positions", torch.int32, (T,), dev)
-    _cuda(inv_freq, "inv_freq")
-    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > D:
-        raise ValueError(f"inv_freq must be [rotary / 2] with rotary <= {D} (got {tuple(inv_freq.shape)})")
-    _need(inv_freq, "inv_freq", torch.float32, inv_freq.shape, dev)
+    _need(positions, "positions", _i32, (T,), dev)
+    turned = _tensor(inv_freq, "inv_freq").shape
+    if len(turned) != 1 or 2 * turned[0] > D:
+        raise ValueError(f"inv_freq must be [rotary / 2] with rotary <= {D} (got {tuple(turned)})")
+    _need(inv_freq, "inv_freq", _f32, turned, dev)
     rows = 0
     if (k_cache is None) != (v_cache is None) or (k_cache is None) != (slots is None) or \
             (k_cache is None) != (v is None):
         raise ValueError("k_cache, v_cache, slots and v belong together: give all or none")
     if k_cache is not None:
-        _cuda(k_cache, "k_cache")
-        if k_cache.dim() != 4:
+        cshape = _tensor(k_cache, "k_cache").shape
+        if len(cshape) != 4:
             raise ValueError("k_cache and v_cache must be [P, page_size, Hkv, D]")
-        cshape = (k_cache.shape[0], k_cache.shape[1], Hkv, D)
+        cshape = (cshape[0], cshape[1], Hkv, D)
         _need(v, "v", act, (T, Hkv, D), dev)
         _need(k_cache, "k_cache", act, cshape, dev)
         _need(v_cache, "v_cache", act, cshape, dev)
-        _need(slots, "slots", torch.int32, (T,), dev)
+        _need(slots, "slots", _i32, (T,), dev)
         rows = cshape[0] * cshape[1]
     if q_out is not None:
         _need(q_out, "q_out", act, (T, Hq, D), dev)
@@ -231,11 +237,12 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
         q_out = torch.empty_like(q)
     if k_out is None and k_cache is None:
         k_out = torch.empty_like(k)
-    rc = _layers_lib().gdn_rope_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(positions), _ptr(inv_freq), _ptr(slots), mscale,
-                                    _ptr(q_out), _ptr(k_out), _ptr(k_cache), _ptr(v_cache), T, Hq, Hkv, D,
-                                    2 * inv_freq.shape[0], 1 if interleaved else 0, rows, _b.DTYPES[act],
+    rc = _layers_lib().gdn_rope_fwd(q.data_ptr(), k.data_ptr(), _ptr(v), positions.data_ptr(), inv_freq.data_ptr(),
+                                    _ptr(slots), mscale, q_out.data_ptr(), _ptr(k_out), _ptr(k_cache), _ptr(v_cache),
+                                    T, Hq, Hkv, D, 2 * turned[0], 1 if interleaved else 0, rows, _b.DTYPES[act],
                                     _current_stream(dev))
-    _b._check(rc, "gdn_rope_fwd")
+    if rc:
+        _b._check(rc, "gdn_rope_fwd")
     return q_out, k_out
 
 
@@ -266,12 +273,11 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
             return paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale, max_seqlen, out, lse, output_lse,
                                   workspace)
     act = _act(q, "q", (torch.bfloat16, torch.float16))
-    _cuda(k_cache, "k_cache")
-    _cuda(block_table, "block_table")
-    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+    cshape, tshape = _tensor(k_cache, "k_cache").shape, _tensor(block_table, "block_table").shape
+    if q.dim() != 3 or len(cshape) != 4 or len(tshape) != 2:
         raise ValueError("q must be [B, Hq, D], the caches [P, page_size, Hkv, D] and block_table [B, max_pages]")
     B, Hq, D = q.shape
-    P, page, Hkv, _ = k_cache.shape
+    P, page, Hkv, _ = cshape
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"Hq ({Hq}) must be a multiple of Hkv ({Hkv})")
     if page < 1:
@@ -281,32 +287,33 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
         raise ValueError("max_seqlen must not be negative")
     if scale is not None and not 0.0 < scale < math.inf:
         raise ValueError(f"scale must be positive and finite (got {scale})")
-    max_pages = block_table.shape[1]
+    max_pages = tshape[1]
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _need(k_cache, "k_cache", act, (P, page, Hkv, D), dev)
     _need(v_cache, "v_cache", act, (P, page, Hkv, D), dev)
-    _need(block_table, "block_table", torch.int32, (B, max_pages), dev)
-    _need(seq_lens, "seq_lens", torch.int32, (B,), dev)
+    _need(block_table, "block_table", _i32, (B, max_pages), dev)
+    _need(seq_lens, "seq_lens", _i32, (B,), dev)
     if out is not None:
         _need(out, "out", act, (B, Hq, D), dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (B, Hq), dev)
+        _need(lse, "lse", _f32, (B, Hq), dev)
     if workspace is not None:
         if _cuda(workspace, "workspace") != dev or not workspace.is_contiguous():
             raise RuntimeError(f"workspace must be a contiguous tensor on cuda:{dev}")
     if out is None:
         out = torch.empty_like(q)
     if lse is None and output_lse:
-        lse = q.new_empty((B, Hq), dtype=torch.float32)
+        lse = torch.empty(B, Hq, dtype=_f32, device=q.device)  # (sizes as a tuple take half a microsecond more)
     if workspace is None:
         nbytes = paged_attn_workspace_bytes(B, Hq, Hkv, D, page, max_pages, max_seqlen)
         if nbytes:
-            workspace = q.new_empty((nbytes,), dtype=torch.uint8)
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    rc = _layers_lib().gdn_paged_attn_fwd(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-                                          0.0 if scale is None else scale, _ptr(out), _ptr(lse), B, Hq, Hkv, D, P,
-                                          page, max_pages, max_seqlen, _b.DTYPES[act], _ptr(workspace), ws_bytes,
-                                          _current_stream(dev))
-    _b._check(rc, "gdn_paged_attn_fwd")
+    rc = _layers_lib().gdn_paged_attn_fwd(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                                          seq_lens.data_ptr(), 0.0 if scale is None else scale, out.data_ptr(),
+                                          _ptr(lse), B, Hq, Hkv, D, P, page, max_pages, max_seqlen, _b.DTYPES[act],
+                                          _ptr(workspace), ws_bytes, _current_stream(dev))
+    if rc:
+        _b._check(rc, "gdn_paged_attn_fwd")
     return out, lse

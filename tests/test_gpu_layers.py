@@ -878,3 +878,14 @@ def test_layers_captured_with_copies_and_branches():
         for a, b in zip(got_now, want):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         assert not want[4].any() and torch.isfinite(want[3].float()).all()
+
+
+@pytest.mark.parametrize("quant, scales", [(None, None), ("row", ()), ("block", (3,))])
+def test_norm_of_one_row(quant, scales):
+    """x [width]: the same as a matrix of one row; the scale of a row has no dimension."""
+    g = gen(24)
+    x, w = randn(g, 300), randn(g, 300)
+    out, none, sc = gdn.rms_norm(x, w, quant=quant)
+    want, _, wsc = gdn.rms_norm(x[None], w, quant=quant)
+    assert out.shape == (300,) and none is None and torch.equal(out.view(torch.uint8), want[0].view(torch.uint8))
+    assert sc is None if quant is None else sc.shape == scales and torch.equal(sc, wsc[0])
