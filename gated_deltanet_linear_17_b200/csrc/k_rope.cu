@@ -22,7 +22,7 @@
 //
 // Measured (bf16, 32768 tokens of 16 + 2 heads of 256 with the cache's write): 108 us, 6.2 TB/s, 96 % of the copy
 // rate; with the factors read from shared memory for every head 198 us.  4099 tokens of 32 + 8 heads of 128, pairs,
-// fp16: 16.7 us, 5.0 TB/s, a third of it the kernel's start and end.  64 tokens: 2.8 us.
+// fp16: 15.2 us, 5.5 TB/s, of it 2.5 the kernel's start and end.  64 tokens: 2.8 us.
 #include <algorithm>
 
 #include "gdn_layers.h"
@@ -208,10 +208,12 @@ cudaError_t launch_type(const RopeParams &p, bool interleaved, cudaStream_t st)
 cudaError_t launch_rope(const RopeParams &in, int act_dtype, bool interleaved, cudaStream_t st)
 {
     RopeParams p = in;
-    // split the heads over warps until the warps fill the GPU (148 SMs of three CTAs)
+    // split the heads over warps as long as all CTAs find room at once (148 SMs of three): a second turn of CTAs costs more
+    // than idle warps (2000 tokens of 16 + 2 heads of 256: 7.2 us with 2000 warps, 8.8 with 4000, 10.6 with 8000; 4099 of
+    // 32 + 8 of 128, fp16: 15.2 us with 2050, 16.7 with 4100)
     const int heads = std::max(p.Hq, p.Hkv), per = 32 / (p.D / 8);
     p.split = 1;
-    while (p.split < kRopeWarps && p.split < heads && (p.T + per - 1) / per * p.split < 148 * 3 * kRopeWarps) p.split *= 2;
+    while (p.split < kRopeWarps && p.split < heads && (p.T + per - 1) / per * p.split * 2 <= 148 * 3 * kRopeWarps) p.split *= 2;
     switch (act_dtype) {
     case GDN_DTYPE_BF16: return launch_type<Bf16>(p, interleaved, st);
     case GDN_DTYPE_FP16: return launch_type<F16>(p, interleaved, st);
