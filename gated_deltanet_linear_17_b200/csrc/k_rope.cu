@@ -20,7 +20,7 @@
 // again, from L1).  A warp takes as many tokens as it has room for rows, and reads up to four heads ahead of its
 // work on them; where there are few tokens, several warps share their heads.
 //
-// Measured (bf16, 32768 tokens of 16 + 2 heads of 256 with the cache's write): 108 us, 6.2 TB/s, 96 % of the copy
+// Measured (bf16, 32768 tokens of 16 + 2 heads of 256 with the cache's write): 106 us, 6.3 TB/s, 98 % of the copy
 // rate; with the factors read from shared memory for every head 198 us.  4099 tokens of 32 + 8 heads of 128, pairs,
 // fp16: 15.2 us, 5.5 TB/s, of it 2.5 the kernel's start and end.  64 tokens: 2.8 us.
 #include <algorithm>
@@ -32,7 +32,8 @@ namespace gdn {
 
 namespace {
 
-constexpr int kRopeThreads = 256, kRopeWarps = kRopeThreads / 32, kAhead = 4;
+// 4 warps: with 8 a CTA 2 to 3 % slower at 4000 tokens and more, at the start and end of the grid
+constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32, kAhead = 4;
 enum Layout { kPairs, kHalves, kHalvesUnaligned };
 
 // mscale times the cosine and sine of position * f
@@ -45,8 +46,8 @@ __device__ __forceinline__ float2 turn(int position, float f, float mscale)
     return make_float2(__cosf(r) * mscale, __sinf(r) * mscale);
 }
 
-// CTAs an SM that the registers are cut for: three where nothing is spilled for it
-constexpr int rope_ctas(int size, Layout layout, int dim) { return size == 4 || layout == kHalvesUnaligned || dim == 0 ? 2 : 3; }
+// CTAs an SM that the registers are cut for: six where next to nothing is spilled for it
+constexpr int rope_ctas(int size, Layout layout, int dim) { return size == 4 || layout == kHalvesUnaligned || dim == 0 ? 4 : 6; }
 
 // DIM: the head dimension, or 0 for any other than those built
 template <class A, Layout LAYOUT, int DIM>
@@ -208,12 +209,12 @@ cudaError_t launch_type(const RopeParams &p, bool interleaved, cudaStream_t st)
 cudaError_t launch_rope(const RopeParams &in, int act_dtype, bool interleaved, cudaStream_t st)
 {
     RopeParams p = in;
-    // split the heads over warps as long as all CTAs find room at once (148 SMs of three): a second turn of CTAs costs more
+    // split the heads over warps as long as all CTAs find room at once (148 SMs of six): a second turn of CTAs costs more
     // than idle warps (2000 tokens of 16 + 2 heads of 256: 7.2 us with 2000 warps, 8.8 with 4000, 10.6 with 8000; 4099 of
     // 32 + 8 of 128, fp16: 15.2 us with 2050, 16.7 with 4100)
     const int heads = std::max(p.Hq, p.Hkv), per = 32 / (p.D / 8);
     p.split = 1;
-    while (p.split < kRopeWarps && p.split < heads && (p.T + per - 1) / per * p.split * 2 <= 148 * 3 * kRopeWarps) p.split *= 2;
+    while (p.split < kRopeWarps && p.split < heads && (p.T + per - 1) / per * p.split * 2 <= 148 * 6 * kRopeWarps) p.split *= 2;
     switch (act_dtype) {
     case GDN_DTYPE_BF16: return launch_type<Bf16>(p, interleaved, st);
     case GDN_DTYPE_FP16: return launch_type<F16>(p, interleaved, st);
