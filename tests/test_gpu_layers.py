@@ -889,3 +889,38 @@ def test_norm_of_one_row(quant, scales):
     want, _, wsc = gdn.rms_norm(x[None], w, quant=quant)
     assert out.shape == (300,) and none is None and torch.equal(out.view(torch.uint8), want[0].view(torch.uint8))
     assert sc is None if quant is None else sc.shape == scales and torch.equal(sc, wsc[0])
+
+
+def test_layers_from_two_threads():
+    """Two host threads, a stream and inputs each: the calls share nothing."""
+    import threading
+
+    f, _ = gdn.rope_inv_freq(64)
+    sets = []
+    for i in (0, 1):
+        g = gen(25 + i)
+        c = Paged([4000 + i, 33], 2, 128, 16, BF16, seed=10 + i)
+        sets.append((c, randn(g, 2, 8, 128), randn(g, 2, 2, 128), randn(g, 64, 1000 + 24 * i), randn(g, 1000 + 24 * i),
+                     torch.tensor([3999 + i, 32], dtype=torch.int32, device="cuda")))
+
+    def step(c, q, k, x, w, pos):
+        turned, _ = gdn.rope_fwd(q, k, pos, f)
+        return (gdn.rms_norm(x, w, quant="row")[0].view(torch.uint8), turned,
+                gdn.paged_attn_fwd(turned, c.k, c.v, c.table, c.seq_lens)[0])
+
+    want = [step(*s) for s in sets]
+    torch.cuda.synchronize()
+    same = [0, 0]
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(50):
+                got = step(*sets[i])
+                same[i] += all(torch.equal(a, b) for a, b in zip(got, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert same == [50, 50]
