@@ -488,25 +488,51 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
     }
 }
 
+// The dynamic shared memory of a launch that reads this many matrices, and whether it holds two stages of a row.
+struct NormSmem {
+    int bytes;
+    bool two_stages;
+};
+constexpr int norm_beside(Kind kind, int L, int PER)  // the static part, and the driver's KB
+{
+    return 1280 + (kind == kShifted ? norm_block(L) * PER / 16 : 0);
+}
+template <class A>
+constexpr NormSmem norm_smem(Kind kind, int L, int PER, int matrices)
+{
+    const int stage = norm_ring<A>(L, PER) ? norm_block(L) * PER * (int)sizeof(typename A::raw) * matrices : 0;
+    const int one = norm_weight_bytes<A>(kind, L, PER) + stage;
+    const bool two = norm_two_stages(kind, L) && kNormSmem / (one + stage + norm_beside(kind, L, PER)) >= norm_ctas(L);
+    return NormSmem{two ? one + stage : one, two};
+}
+template <class A>
+constexpr int norm_smem_most(Kind kind, int L, int PER)  // of all launches of an instance
+{
+    int most = 0;
+    for (int matrices = 1; matrices <= 3; ++matrices)
+        if (norm_smem<A>(kind, L, PER, matrices).bytes > most) most = norm_smem<A>(kind, L, PER, matrices).bytes;
+    return most;
+}
+
 template <class A, Kind KIND, int L, int PER>
 cudaError_t launch_kernel(const NormParams &p, cudaStream_t st)
 {
     NormParams q = p;
     const auto kern = rms_norm_kernel<A, KIND, L, PER>;
-    constexpr int block = norm_block(L), rows = L <= 32 ? block / L : 1;
-    const int matrices = 1 + (p.residual != nullptr) + (p.gate != nullptr);
-    const size_t beside = 1280 + (KIND == kShifted ? block * PER / 16 : 0);  // the static part, and the driver's KB
-    const size_t stage = norm_ring<A>(L, PER) ? (size_t)block * PER * sizeof(typename A::raw) * matrices : 0;
-    size_t smem = norm_weight_bytes<A>(KIND, L, PER) + stage;
-    q.two_stages = norm_two_stages(KIND, L) && (int)(kNormSmem / (smem + stage + beside)) >= norm_ctas(L);
-    if (q.two_stages) smem += stage;
-    if (smem > 47 * 1024) {  // 48 KB with the static part
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr int block = norm_block(L), rows = L <= 32 ? block / L : 1, beside = norm_beside(KIND, L, PER);
+    const NormSmem smem = norm_smem<A>(KIND, L, PER, 1 + (p.residual != nullptr) + (p.gate != nullptr));
+    q.two_stages = smem.two_stages;
+    // The limit belongs to the kernel, not to the launch, and host threads share it: every call sets it to the same value,
+    // so that none takes from another between its setting and its launch.
+    constexpr int most = norm_smem_most<A>(KIND, L, PER);
+    static_assert(most + beside <= kNormSmem, "a row's matrices fit into an SM");
+    if (most > 47 * 1024) {  // 48 KB with the static part
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
-    const int per_sm = std::max(1, std::min(norm_ctas(L), (int)(kNormSmem / (smem + beside))));
+    const int per_sm = std::max(1, std::min(norm_ctas(L), kNormSmem / (smem.bytes + beside)));
     const long long want = (p.rows + rows - 1) / rows;
-    return launch_early(kern, (unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem, st, q);
+    return launch_early(kern, (unsigned)std::min<long long>(want, (long long)kNormSms * per_sm), block, smem.bytes, st, q);
 }
 
 // The threads of a row: the fewest of those built that hold `places` places, at least `least`.  A thread holds 32
