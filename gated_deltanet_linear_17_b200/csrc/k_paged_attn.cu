@@ -25,7 +25,9 @@
 // maximum, sum and output accumulators (fp32, in registers), no CTA barrier.  At the end of a piece the
 // warps' results are joined through shared memory, while the next piece's tiles are on their way.
 //
-// Roundings.  Scores, exponentials (base 2, the scale folded in), sums and outputs are fp32.  The
+// Roundings.  Scores, exponentials, sums and outputs are fp32.  An exponential's argument is a score's distance from the
+// maximum, times scale log2 e: the maximum's own is exactly 0 however large the scores are.  (A fused score * scale - ref
+// is off by up to |ref| 2^-24 there, which leaves the range of an exponent from |ref| of 2^31 on.)  The
 // probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
 // p in bf16, 22 in fp16): one rounded number would put an error as large as the output's own rounding
 // into it, and the second product costs nothing beside the memory traffic.  The sum of exponentials
@@ -188,14 +190,14 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t a)
     return v;
 }
 
-// 4 columns from 4 c on of one query head's output, x unnormalised, and its lse
+// 4 columns from 4 c on of one query head's output, x unnormalised, and its lse; top: the maximum, unscaled
 template <int D, bool F16>
 __device__ __forceinline__ void write_out(const AttnParams &p, long long head, int c, float4 x, float top, float sum)
 {
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + head * D + 4 * c) =
         make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-    if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * (top + log2f(sum));
+    if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * fmaf(top, p.scale_log2, log2f(sum));
 }
 
 // One piece of a CTA's work: keys [k0, k1) of head group `pair` of sequence b (of the list, `take` places from u0
@@ -444,18 +446,16 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
                     for (int e = 0; e < 2 * NT; ++e)
                         if (8 * t + 2 * (lane & 3) + (e & 1) >= left) s[t][e] = -INFINITY;
             }
-            // maxima of the scores as they are (the scale is positive); m and ref scaled, in base 2
-            float alpha[NT], ref[NT];
+            float alpha[NT], ref[NT];  // maxima are of the scores as they are (the scale is positive)
             bool moved = false;
 #pragma unroll
             for (int r = 0; r < NT; ++r) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int t = 0; t < 2 * kSteps; ++t) top = fmaxf(top, fmaxf(s[t][2 * r], s[t][2 * r + 1]));
-                top = quad_max(top) * p.scale_log2;
-                const float most = fmaxf(m[r], top);
+                const float most = fmaxf(m[r], quad_max(top));
                 ref[r] = most == -INFINITY ? 0.f : most;  // every score -infinity so far: the exponentials are 0
-                alpha[r] = ex2(m[r] - ref[r]);
+                alpha[r] = ex2((m[r] - ref[r]) * p.scale_log2);
                 moved |= alpha[r] != 1.f;
                 m[r] = most;
                 l[r] *= alpha[r];
@@ -481,8 +481,9 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int r = 0; r < NT; ++r)
 #pragma unroll
                 for (int t = 0; t < 2 * kSteps; ++t) {
-                    const float p0 = ex2(fmaf(s[t][2 * r], p.scale_log2, -ref[r]));
-                    const float p1 = ex2(fmaf(s[t][2 * r + 1], p.scale_log2, -ref[r]));
+                    const float2 below = fadd2(make_float2(s[t][2 * r], s[t][2 * r + 1]), make_float2(-ref[r], -ref[r]));
+                    const float2 x = fmul2(below, make_float2(p.scale_log2, p.scale_log2));
+                    const float p0 = ex2(x.x), p1 = ex2(x.y);
                     l[r] += p0 + p1;
                     split2<F16>(p0, p1, hi[r][t], lo[r][t]);
                 }
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int e = 0; e < 2; ++e) {
                 const int row = 8 * r + 2 * (lane & 3) + e;
                 if (row >= rows) continue;
-                const float f = ex2(wm[warp][row] - top_of(row));
+                const float f = ex2((wm[warp][row] - top_of(row)) * p.scale_log2);
 #pragma unroll
                 for (int t = 0; t < D / 16; ++t) {
                     os[swizzled(row, 16 * t + lane / 4)] = o[t][r][e] * f;
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             for (int w = 0; w < kWarps; ++w) {
                 const float4 y = *reinterpret_cast<const float4 *>(sums(w) + at);
                 x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                sum += wl[w][row] * ex2(wm[w][row] - top);
+                sum += wl[w][row] * ex2((wm[w][row] - top) * p.scale_log2);
             }
             if (whole) {
                 write_out<D, F16>(p, (long long)now.b * p.Hq + head0 + row, c, x, top, sum);
@@ -599,7 +600,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 #pragma unroll
                 for (int r = 0; r < kAttnMaxCluster; ++r) {
                     if (r >= p.direct) break;
-                    const float w = ex2(part_ml[r].x - top);
+                    const float w = ex2((part_ml[r].x - top) * p.scale_log2);
                     sum = fmaf(w, part_ml[r].y, sum);
                     x.x = fmaf(w, part_x[r].x, x.x), x.y = fmaf(w, part_x[r].y, x.y);
                     x.z = fmaf(w, part_x[r].z, x.z), x.w = fmaf(w, part_x[r].w, x.w);
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
         top = top == -INFINITY ? 0.f : top;
-        const float w = ex2(ml.x - top), sum = warp_sum(w * ml.y);
+        const float w = ex2((ml.x - top) * p.scale_log2), sum = warp_sum(w * ml.y);
 #pragma unroll
         for (int i = 0; i < kPerLane; ++i) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -753,11 +754,11 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
             }
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) now = fmaxf(now, ml[i].x);
-            const float ref = now == -INFINITY ? 0.f : now, keep = ex2(top - ref);
+            const float ref = now == -INFINITY ? 0.f : now, keep = ex2((top - ref) * p.scale_log2);
             x.x *= keep, x.y *= keep, x.z *= keep, x.w *= keep, sum *= keep;
 #pragma unroll
             for (int i = 0; i < kInFlight; ++i) {
-                const float w = ex2(ml[i].x - ref);
+                const float w = ex2((ml[i].x - ref) * p.scale_log2);
                 sum = fmaf(w, ml[i].y, sum);
                 x.x = fmaf(w, y[i].x, x.x), x.y = fmaf(w, y[i].y, x.y);
                 x.z = fmaf(w, y[i].z, x.z), x.w = fmaf(w, y[i].w, x.w);
@@ -776,7 +777,7 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 const float4 y = part[i][tid];
-                const float w = ex2(part_ml[i].x - top);
+                const float w = ex2((part_ml[i].x - top) * p.scale_log2);
                 sum = fmaf(w, part_ml[i].y, sum);
                 x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
             }

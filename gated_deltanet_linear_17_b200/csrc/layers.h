@@ -121,7 +121,7 @@ struct AttnParams {
     float *lse;
     int4 *begun;      // [ctas]: sequence, first query head, query heads and pieces of the pair that a CTA began and
                       // did not finish (pieces 0: none)
-    float2 *part_ml;  // [ctas][2][16]: a piece's maximum (base 2) and sum of exponentials
+    float2 *part_ml;  // [ctas][2][16]: a piece's maximum (unscaled) and sum of exponentials
     float *part;      // [ctas][2][16][D]: its unnormalised sum
     float scale_log2;
     int B, Hq, Hkv, group, row_tiles, P, page_size, max_pages, ctas, direct;

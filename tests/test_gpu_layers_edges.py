@@ -9,12 +9,11 @@ import threading
 import pytest
 import torch
 
+import gated_deltanet_linear_17_b200 as gdn
 from gated_deltanet_linear_17_b200 import _layers
-from test_gpu_layers import F32, BF16, gen, norm64, randn, within
+from test_gpu_layers import BF16, F16, F32, HALF, TINY, Paged, attn64, gen, norm64, randn, within
 
 pytestmark = pytest.mark.gpu
-
-HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 
 
 # ------------------------------------------------------------------ norm
@@ -53,3 +52,41 @@ def test_norm_of_two_sizes_from_two_threads(width, dtype):
     for (x, w, r), (out, _) in zip(ins, outs):
         _, y = norm64(x, w, r, None, 1e-6, 0.0)
         within(out, y, (HALF[dtype] + 2.0 ** -17) * y.abs(), "out")
+
+
+# ------------------------------------------------------------------ paged attention
+
+
+def set_rows(c, b, k=None, v=None):
+    """Sequence b's keys (values) [n, Hkv, D] into its list and its pages."""
+    j = torch.arange(c.lens[b], device="cuda")
+    rows = c.table[b].long()[j // c.page] * c.page + j % c.page
+    for new, mine, cache in ((k, c.keys, c.k), (v, c.values, c.v)):
+        if new is not None:
+            mine[b] = new
+            cache.view(-1, *cache.shape[2:])[rows] = new
+
+
+@pytest.mark.parametrize("dtype, size", [(F16, 2000.0), (F16, 20000.0), (F16, 60000.0), (BF16, 1e8), (BF16, 1e15)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n, columns", [(1, None), (40, None), (3000, None), (3000, 100000)])
+def test_attn_scores_of_extreme_size(dtype, size, D, n, columns):
+    """Scores of up to some 10^31, of either sign.  Two keys (one, of a single key) share the largest score, every other
+    lies below it by more than an exponential's range.  The two scores come of the same numbers by the same steps, so
+    they are equal, their weights 1 and all others 0: out is the mean of the two values, off by its own rounding and one
+    in fp32.  The magnitudes of a score add up to |lse|, and its D / 16 + 4 steps are good to 2^-22 each."""
+    c = Paged([n, n], 1, D, 16, dtype, seed=int(size) % 97)
+    top = sorted({min(7, n - 1), n * 5 // 6})
+    q = torch.full((2, 3, D), size, device="cuda", dtype=dtype)
+    for b, (high, low) in enumerate(((1.0, 0.0), (-0.5, -1.0))):
+        k = torch.full((n, 1, D), low, device="cuda") * size
+        k[top] = high * size
+        set_rows(c, b, k=k.to(dtype))
+    if columns:
+        c = c.widened(columns)
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, output_lse=True)
+    for b in range(2):
+        o = c.values[b][top].double().mean(0).expand(3, D)
+        _, l, _, _ = attn64(q[b], c.keys[b], c.values[b], D ** -0.5)
+        within(out[b], o, (HALF[dtype] + 2.0 ** -24) * o.abs() + TINY[dtype], "out")
+        within(lse[b], l, ((D / 16 + 4) * 2.0 ** -22 + 2.0 ** -20) * l.abs(), "lse")
