@@ -31,7 +31,11 @@
 // probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
 // p in bf16, 22 in fp16): one rounded number would put an error as large as the output's own rounding
 // into it, and the second product costs nothing beside the memory traffic.  The sum of exponentials
-// takes them unrounded, so lse is good to fp32.
+// takes them unrounded, so lse is good to fp32.  The tensor core cuts off what an addition to its accumulator drops
+// (up to 2^-23 of the accumulator, always towards zero), so no more than 512 additions (256 tiles of 16 keys) go to one: a
+// piece of the list ends after kMostKeys keys, and the CTA adds its pieces of a pair up in fp32, rounded; a cluster's CTA that
+// gets more keys than its hint said sums a tile's products on their own and adds them so.  (300 rows over 131072 keys of
+// positive values, D = 256: on average 8e-5 too small, without that 3.2e-4; over 10^6 keys, D = 128, 4e-5 against 1.5e-3.)
 //
 // Measured (bf16): 256 sequences of 1024 to 16384 keys, 16 / 2 heads of 256: 692 us, 6.8 TB/s (a read-only stream
 // passes the copy rate); 64 of 1 to 8192 keys, 32 / 8 heads of 128: 172 us, 6.4 TB/s; one of 131072 keys, 16 / 2
@@ -56,6 +60,7 @@ struct Shape {
     static constexpr int kSteps = kTile / 16;        // for what a tile costs beside them (16 sequences of 8 heads, up
                                                      // to 8000 keys: 39 us with 16, 36 us with 32)
     static constexpr int kCtas = DIRECT ? kDirectCtasPerSm(D) : kAttnCtasPerSm;
+    static constexpr int kChain = 256 / kSteps;      // tiles whose products go to one accumulator
     static constexpr int kStages = 3;
     static constexpr int kHalf = kTile * D * 2;      // bytes of a tile's keys (or values)
     static constexpr int kStage = 2 * kHalf;
@@ -118,11 +123,10 @@ struct Part {
 // All threads call it.  Thread t sums the places of its run of sequences; a scan over the threads finds the
 // run that holds the CTA's first place, and the run's thread the sequence.
 template <int D, int kThreads>
-__device__ __forceinline__ Part find_part(const AttnParams &p)
+__device__ __forceinline__ void find_part(const AttnParams &p, Part &found)  // (in shared memory)
 {
     constexpr int kWarps = kThreads / 32;
     __shared__ long long warp_total[kWarps];
-    __shared__ Part found;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int run = (p.B + kThreads - 1) / kThreads, b0 = min(tid * run, p.B), b1 = min(b0 + run, p.B);
     const int heads = p.Hkv * p.row_tiles;
@@ -163,7 +167,6 @@ __device__ __forceinline__ Part find_part(const AttnParams &p)
     }
     if (tid == 0 && i >= ctas) found.ctas = ctas;
     __syncthreads();
-    return found;
 }
 
 __device__ __forceinline__ void cluster_arrive_wait()
@@ -201,16 +204,19 @@ __device__ __forceinline__ void write_out(const AttnParams &p, long long head, i
 }
 
 // One piece of a CTA's work: keys [k0, k1) of head group `pair` of sequence b (of the list, `take` places from u0
-// on), and how many places of the CTA's part lie behind it.
+// on), and how many places of the CTA's part lie behind it.  `from`: the place at which the CTA began the pair, before u0
+// where the pair's keys are more than one piece here.
+template <int D>
+constexpr int kMostKeys = D == 256 ? 8192 : 16384;  // 512 additions to an accumulator in 2 (4) warps
 struct Piece {
     int b, pair, n, n_next;  // n: the sequence's length as given, n_next: of the sequence behind it
-    int u0, take, k0, k1;
+    int u0, take, k0, k1, from;
     long long left;
 };
 template <int D>
 __device__ __forceinline__ void cut(Piece &c, const AttnParams &p)  // the piece that begins at u0
 {
-    c.take = (int)min(c.left, (long long)(attn_places(D, c.n, p.capacity) - c.u0));
+    c.take = (int)min(c.left, (long long)min(kMostKeys<D> / kAttnUnit, attn_places(D, c.n, p.capacity) - c.u0));
     c.left -= c.take;
     const KeyRange k = attn_keys(D, c.u0, c.take, attn_refused(c.n, p.capacity) ? 0 : c.n);
     c.k0 = k.k0;
@@ -219,7 +225,12 @@ __device__ __forceinline__ void cut(Piece &c, const AttnParams &p)  // the piece
 template <int D>
 __device__ __forceinline__ void next_piece(Piece &c, const AttnParams &p, int heads)
 {
-    c.u0 = 0;
+    c.u0 += c.take;
+    if (c.u0 < attn_places(D, c.n, p.capacity)) {
+        cut<D>(c, p);
+        return;
+    }
+    c.u0 = c.from = 0;
     if (++c.pair == heads) {
         c.pair = 0;
         ++c.b;
@@ -242,6 +253,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     __shared__ float wm[kWarps][kRows], wl[kWarps][kRows];
     __shared__ int wslot[kWarps];     // the stage that holds a warp's sums while the warps are joined
     __shared__ float2 joined[kRows];  // DIRECT: maximum and sum of this CTA's part of the keys
+    __shared__ float2 carried[2][kRows];  // of the pair's pieces so far, to one half and from the other in turn
     begin_early();
     if (!DIRECT) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join's small CTAs
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -251,7 +263,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
     const int heads = p.Hkv * p.row_tiles;
 
     Piece now;
-    Part part = {};
+    __shared__ Part part;
     const int rank = DIRECT ? (int)blockIdx.x % p.direct : 0;
     if (DIRECT) {
         const int at = (int)blockIdx.x / p.direct;
@@ -261,9 +273,9 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         const KeyRange k = attn_cluster_keys(rank, p.direct, attn_refused(now.n, p.capacity) ? 0 : now.n);
         now.k0 = k.k0;
         now.k1 = k.k1;
-        now.left = now.n_next = now.u0 = now.take = 0;
+        now.left = now.n_next = now.u0 = now.take = now.from = 0;
     } else {
-        part = find_part<D, kThreads>(p);
+        find_part<D, kThreads>(p, part);
         if ((int)blockIdx.x >= part.ctas) {
             if (tid == 0) p.begun[blockIdx.x] = make_int4(0, 0, 0, 0);
             return;
@@ -272,7 +284,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         now.pair = part.pair;
         now.n = part.n;
         now.n_next = now.b + 1 < p.B ? p.lens[now.b + 1] : 0;
-        now.u0 = part.u0;
+        now.u0 = now.from = part.u0;
         now.left = part.last - part.first;
         cut<D>(now, p);
     }
@@ -380,14 +392,11 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         }
     };
 
-    long long pos = part.first;  // of the list: the piece's first place
-    int4 begun = make_int4(0, 0, 0, 0);
     int stage = 0;  // of this warp's next tile; the one before it is free
+    int turn = 0;   // of the halves of `carried`
     for (;;) {
         const int hkv = now.pair / p.row_tiles, row0 = (now.pair - hkv * p.row_tiles) * kRows;
         const int rows = min(kRows, p.group - row0), head0 = hkv * p.group + row0;
-        const int all = DIRECT ? 0 : attn_places(D, now.n, p.capacity);
-        const bool whole = DIRECT ? p.direct == 1 : now.take == all;
 
         // o: the output transposed, o[t][r][e] at column 16 t + lane / 4 (+ 8 for e >= 2) of query row
         // 8 r + 2 (lane % 4) (+ 1 for odd e); m, l: of query row 8 r + lane / 4 (l this lane's part of the sum)
@@ -487,19 +496,44 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
                     l[r] += p0 + p1;
                     split2<F16>(p0, p1, hi[r][t], lo[r][t]);
                 }
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
+            // 16 columns of the output
+            auto add_products = [&](int t, float (&x)[NT][4]) {
 #pragma unroll
                 for (int h = 0; h < kSteps; ++h) {
                     uint32_t a[4];
                     ldsm_x4_t(vs + sw<D>(16 * h + (lane & 7) + ((lane >> 4) << 3), 2 * t + ((lane >> 3) & 1)), a[0],
                               a[1], a[2], a[3]);
 #pragma unroll
-                    for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, hi[r][2 * h], hi[r][2 * h + 1]);
+                    for (int r = 0; r < NT; ++r) mma<F16>(x[r], a, hi[r][2 * h], hi[r][2 * h + 1]);
 #pragma unroll
-                    for (int r = 0; r < NT; ++r) mma<F16>(o[t][r], a, lo[r][2 * h], lo[r][2 * h + 1]);
+                    for (int r = 0; r < NT; ++r) mma<F16>(x[r], a, lo[r][2 * h], lo[r][2 * h + 1]);
                 }
+            };
+            if (!DIRECT || __builtin_expect(mine <= S::kChain, 1)) {
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) add_products(t, o[t]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) {
+                    float x[NT][4] = {};
+                    add_products(t, x);
+#pragma unroll
+                    for (int r = 0; r < NT; ++r)
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 sum = fadd2(make_float2(o[t][r][e], o[t][r][e + 1]), make_float2(x[r][e], x[r][e + 1]));
+                            o[t][r][e] = sum.x;
+                            o[t][r][e + 1] = sum.y;
+                        }
+                }
+            }
         }
+
+        const int all = DIRECT ? 0 : attn_places(D, now.n, p.capacity);
+        // the CTA's last piece of the pair; all of the pair in this CTA; pieces of the pair before this one
+        const bool done = DIRECT || now.left == 0 || now.u0 + now.take == all;
+        const bool whole = DIRECT ? p.direct == 1 : now.from == 0 && now.u0 + now.take == all;
+        const bool carries = !DIRECT && now.u0 != now.from;
 
         // The end of the piece: join the warps.  A warp's sums go to its free stage; the next piece's queries are on
         // their way meanwhile.
@@ -555,7 +589,7 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
         __syncthreads();
         for (int i = tid; i < rows * (D / 4); i += kThreads) {
             const int row = i / (D / 4), c = i % (D / 4), at = swizzled(row, 4 * c);
-            const float top = top_of(row);
+            float top = top_of(row);
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             float sum = 0.f;
 #pragma unroll
@@ -564,16 +598,31 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
                 x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
                 sum += wl[w][row] * ex2((wm[w][row] - top) * p.scale_log2);
             }
-            if (whole) {
+            // place 1: the pair begins here; place 0: it began in an earlier CTA.  (Place 1 is free while whole pairs carry
+            // their sums there: the piece that it is for is the part's last.)
+            const long long to = (2LL * blockIdx.x + (now.from == 0)) * 16 + row;
+            float4 *const sum_at = reinterpret_cast<float4 *>(p.part + to * D) + c;  // (DIRECT: not used)
+            if (carries) {
+                const float2 ml = carried[turn][row];
+                const float4 y = *sum_at;
+                const float both = fmaxf(ml.x, sum == 0.f ? -INFINITY : top), ref = both == -INFINITY ? 0.f : both;
+                const float f = sum == 0.f ? 0.f : ex2((top - ref) * p.scale_log2), g = ex2((ml.x - ref) * p.scale_log2);
+                x.x = fmaf(y.x, g, x.x * f), x.y = fmaf(y.y, g, x.y * f);
+                x.z = fmaf(y.z, g, x.z * f), x.w = fmaf(y.w, g, x.w * f);
+                sum = fmaf(ml.y, g, sum * f);
+                top = ref;
+            }
+            if (!done) {
+                *sum_at = x;
+                if (c == 0) carried[turn ^ 1][row] = make_float2(sum == 0.f ? -INFINITY : top, sum);
+            } else if (whole) {
                 write_out<D, F16>(p, (long long)now.b * p.Hq + head0 + row, c, x, top, sum);
             } else if (DIRECT) {
                 *reinterpret_cast<float4 *>(sums(0) + at) = x;  // where this thread read the first warp's part
                 if (c == 0) joined[row] = make_float2(sum == 0.f ? -INFINITY : top, sum);
             } else {
-                // place 1: the pair begins here; place 0: it began in an earlier CTA.  A piece without a weight has
-                // no maximum either: its stand-in 0 would drown scores far below it
-                const long long to = (2LL * blockIdx.x + (now.u0 == 0)) * 16 + row;
-                reinterpret_cast<float4 *>(p.part + to * D)[c] = x;
+                // a piece without a weight has no maximum either: its stand-in 0 would drown scores far below it
+                *sum_at = x;
                 if (c == 0) p.part_ml[to] = make_float2(sum == 0.f ? -INFINITY : top, sum);
             }
         }
@@ -610,18 +659,21 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
             cluster_arrive_wait();  // no CTA leaves while another reads its shared memory
             return;
         }
-        if (!whole && now.u0 == 0) {
-            // the CTA that holds the pair's last place
-            const int until = attn_part_of(part.total, pos + all - 1, part.ctas);
-            begun = make_int4(now.b, head0, rows, until - (int)blockIdx.x + 1);
+        if (last) {
+            // a pair that begins here and goes on in other CTAs is the part's last; the CTA that holds its last place
+            int4 begun = make_int4(0, 0, 0, 0);
+            if (!whole && now.from == 0) {
+                const int until = attn_part_of(part.total, part.last - (now.u0 + now.take) + all - 1, part.ctas);
+                begun = make_int4(now.b, head0, rows, until - (int)blockIdx.x + 1);
+            }
+            if (tid == 0) p.begun[blockIdx.x] = begun;
+            break;
         }
-        if (last) break;
-        pos += now.take;
+        turn ^= 1;
         now = next;
         __syncthreads();  // the free stages, wm, wl and wslot are free again
     }
     cp_async_wait<0>();
-    if (tid == 0) p.begun[blockIdx.x] = begun;
 }
 
 // Joins the pieces of every pair that a CTA of the first kernel began and did not finish: piece 0 lies in

@@ -4,6 +4,7 @@ test_gpu_layers.py; what a test adds to them stands in its docstring."""
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
 
 import pytest
@@ -90,3 +91,96 @@ def test_attn_scores_of_extreme_size(dtype, size, D, n, columns):
         _, l, _, _ = attn64(q[b], c.keys[b], c.values[b], D ** -0.5)
         within(out[b], o, (HALF[dtype] + 2.0 ** -24) * o.abs() + TINY[dtype], "out")
         within(lse[b], l, ((D / 16 + 4) * 2.0 ** -22 + 2.0 ** -20) * l.abs(), "lse")
+
+
+def shared(n, rows, D, dtype, seed, lens=None, columns=None):
+    """`rows` sequences on the same pages, the first `lens[b]` keys of n each (all by default); values of one sign."""
+    g = gen(seed)
+    c = Paged([n], 1, D, 64, dtype, seed=seed, spare=0)
+    set_rows(c, 0, v=(0.75 + 0.5 * torch.rand(n, 1, D, generator=g, device="cuda")).to(dtype))
+    lens = [n] * rows if lens is None else lens
+    table = c.table.expand(len(lens), -1).contiguous()
+    if columns:
+        wide = torch.full((len(lens), columns), -7, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        table = wide
+    return c, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), randn(g, len(lens), 4, D, dtype=dtype)
+
+
+def check_shared(c, table, lens, q, **kw):
+    """All rows against 64 bits.  No more than 512 additions go to one accumulator, each cut off by up to 2^-23 of it: 2^-14
+    more than check_attn allows."""
+    dt, D = q.dtype, q.shape[2]
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, table, lens, output_lse=True, **kw)
+    k, v = c.keys[0][:, 0].double(), c.values[0][:, 0].double()
+    for b0 in range(0, q.shape[0], 50):
+        qq, n = q[b0:b0 + 50].double(), lens[b0:b0 + 50]
+        s = qq @ k.T * D ** -0.5
+        s.masked_fill_(torch.arange(k.shape[0], device="cuda") >= n[:, None, None], -math.inf)
+        e = (D / 16 + 4) * 2.0 ** -22 * (qq.abs() @ k.abs().T).amax(-1) * D ** -0.5
+        l = torch.logsumexp(s, -1)
+        p = torch.exp(s - l[..., None])
+        o = p @ v
+        tol = (2 * e[..., None] + 2.0 ** -13) * (p @ v.abs()) + HALF[dt] * o.abs() + TINY[dt]
+        within(out[b0:b0 + 50], o, tol, f"out of rows {b0} on")
+        within(lse[b0:b0 + 50], l, e + 2.0 ** -20 * (l.abs() + 1), "lse")
+    return out, lse
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("rows, hint", [(300, 0), (300, 1), (3, 1)])
+def test_attn_sums_of_many_keys(D, dtype, rows, hint):
+    """131072 keys a CTA and more, all values positive: what the tensor core cuts off of every addition adds up.  By the
+    list, and by clusters whose hint is far too small."""
+    c, table, lens, q = shared(131072 + 77, rows, D, dtype, D)
+    a = check_shared(c, table, lens, q, max_seqlen=hint)
+    again = gdn.paged_attn_fwd(q, c.k, c.v, table, lens, output_lse=True, max_seqlen=hint)
+    assert torch.equal(a[0], again[0]) and torch.equal(a[1], again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group", [1, 12])
+def test_attn_long_pieces_among_short_ones(D, group):
+    """Lengths around whole pieces (8192 keys at D = 256, else 16384), several sequences a CTA: pieces that begin, end and
+    lie within a CTA's part of the list, with sums carried on from piece to piece; queries of 1 and 12 heads."""
+    some = [8192, 16383, 16385, 0, 16384, 1, 24640, 40000, 7000, 32769, 16320, 16448, 64, 49152, 0, 20001]
+    lens = [some[(3 * i + i // 16) % 16] for i in range(500)]
+    c, table, lens, _ = shared(50000, 0, D, BF16, D + 1, lens=lens)
+    q = randn(gen(D), len(lens), group, D)
+    keep = lens > 0
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, table, lens, output_lse=True)
+    assert (out[~keep] == 0).all() and (lse[~keep] == -math.inf).all()
+    check_shared(c, table[keep], lens[keep], q[keep])
+    check_shared(c, table[keep], lens[keep], q[keep], max_seqlen=64)
+
+
+@pytest.mark.parametrize("hint", [0, 1])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attn_carried_sums_of_every_kind(D, hint):
+    """Pieces without a weight (scores of -infinity), with all of it, with scores far below zero, and with a NaN or a bad
+    page in one of them: of many rows on the same pages, so that a CTA has a sequence to itself."""
+    n, copies = 40000, 60
+    c = Paged([n] * 6, 1, D, 64, BF16, seed=3)
+    q = 1 + 0.1 * randn(gen(4), 6, 2, D).abs()
+    keys = [k.clone() for k in c.keys]
+    keys[0][:18000] = -math.inf
+    keys[1][8000:] = -math.inf
+    keys[2][:] = -math.inf
+    keys[3] = -200 - keys[3].abs()
+    keys[5][20000, 0, 5] = math.nan
+    for b, k in enumerate(keys):
+        set_rows(c, b, k=k)
+    c.table[4, 20000 // 64] = -1
+    q, table, lens = q.repeat(copies, 1, 1), c.table.repeat(copies, 1), c.seq_lens.repeat(copies)
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, table, lens, output_lse=True, max_seqlen=hint)
+    # where a sequence is cut differs from copy to copy, what comes out but in the last bits does not
+    for b in range(6 * copies):
+        if b % 6 not in (2, 4, 5):
+            within(out[b], out[b % 6].double(), 2.0 ** -7 * out[b % 6].double().abs() + 2.0 ** -13, "a copy")
+    assert (out[2::6] == 0).all() and (lse[2::6] == -math.inf).all()
+    assert all(out[i::6].isnan().all() and lse[i::6].isnan().all() for i in (4, 5))
+    for b, part in ((0, slice(18000, n)), (1, slice(0, 8000)), (3, slice(0, n))):
+        o, l, av, e = attn64(q[b], c.keys[b][part], c.values[b][part], D ** -0.5)
+        within(out[b], o, (2 * e[:, None] + 2.0 ** -13) * av + HALF[BF16] * o.abs(), f"out {b}")
+        within(lse[b], l, e + 2.0 ** -20 * (l.abs() + 1), f"lse {b}")
