@@ -28,9 +28,11 @@
 // Roundings.  Scores, exponentials, sums and outputs are fp32.  An exponential's argument is a score's distance from the
 // maximum, times scale log2 e: the maximum's own is exactly 0 however large the scores are.  (A fused score * scale - ref
 // is off by up to |ref| 2^-24 there, which leaves the range of an exponent from |ref| of 2^31 on.)  The
-// probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo (16 bits or more of
-// p in bf16, 22 in fp16): one rounded number would put an error as large as the output's own rounding
-// into it, and the second product costs nothing beside the memory traffic.  The sum of exponentials
+// probabilities enter their product with V as a pair of 16-bit numbers, p = hi + lo: one rounded number would put an error
+// as large as the output's own rounding into it, and the second product costs nothing beside the memory traffic.  In bf16
+// the pair holds 16 bits or more of p, whatever its size.  fp16 ends at 2^-24, so there every weight is 2^15 p (kRaise; up
+// to 32768), and the pair is good to 22 bits or 2^-25, which is 2^-40 of the largest weight: 16 bits of a key that lies 16.6
+// nats below the largest score, 11 bits at 20.  The sum of exponentials
 // takes them unrounded, so lse is good to fp32.  The tensor core cuts off what an addition to its accumulator drops
 // (up to 2^-23 of the accumulator, always towards zero), so no more than 512 additions (256 tiles of 16 keys) go to one: a
 // piece of the list ends after kMostKeys keys, and the CTA adds its pieces of a pair up in fp32, rounded; a cluster's CTA that
@@ -193,6 +195,10 @@ __device__ __forceinline__ float2 cluster_load2(uint32_t a)
     return v;
 }
 
+// the power of two that weights (and with them sums of weights and of values) are raised by
+template <bool F16>
+constexpr float kRaise = F16 ? 15.f : 0.f;
+
 // 4 columns from 4 c on of one query head's output, x unnormalised, and its lse; top: the maximum, unscaled
 template <int D, bool F16>
 __device__ __forceinline__ void write_out(const AttnParams &p, long long head, int c, float4 x, float top, float sum)
@@ -200,7 +206,7 @@ __device__ __forceinline__ void write_out(const AttnParams &p, long long head, i
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + head * D + 4 * c) =
         make_uint2(pack2<F16>(x.x * inv, x.y * inv), pack2<F16>(x.z * inv, x.w * inv));
-    if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * fmaf(top, p.scale_log2, log2f(sum));
+    if (p.lse && c == 0) p.lse[head] = sum == 0.f ? -INFINITY : kLn2 * fmaf(top, p.scale_log2, log2f(sum) - kRaise<F16>);
 }
 
 // One piece of a CTA's work: keys [k0, k1) of head group `pair` of sequence b (of the list, `take` places from u0
@@ -491,7 +497,8 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 #pragma unroll
                 for (int t = 0; t < 2 * kSteps; ++t) {
                     const float2 below = fadd2(make_float2(s[t][2 * r], s[t][2 * r + 1]), make_float2(-ref[r], -ref[r]));
-                    const float2 x = fmul2(below, make_float2(p.scale_log2, p.scale_log2));
+                    const float2 scale = make_float2(p.scale_log2, p.scale_log2);
+                    const float2 x = F16 ? ffma2(below, scale, make_float2(kRaise<F16>, kRaise<F16>)) : fmul2(below, scale);
                     const float p0 = ex2(x.x), p1 = ex2(x.y);
                     l[r] += p0 + p1;
                     split2<F16>(p0, p1, hi[r][t], lo[r][t]);

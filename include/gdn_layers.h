@@ -145,6 +145,8 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  * others are not affected.  NaN and infinities in a sequence's own rows come out
  * as NaN where the formula gives NaN, an infinity in v as an infinity or NaN (p is
  * multiplied in two parts, the second of either sign); cache rows that no sequence lists are never read.
+ * A key's weight is held to 16 bits or more, in fp16 of keys more than 16 nats below the row's largest score to 2^-40 of
+ * the largest weight.
  * q . k is formed in fp32: up to 3.4e38 scores of any size give a right row, beyond it one is an infinity.
  * Alignment: 16 bytes for q, the caches, out and workspace, 4 for the rest.  Errors:
  * GDN_ERR_NULL_ARG, GDN_ERR_BAD_SHAPE, GDN_ERR_UNSUPPORTED (act_dtype, D, P *

@@ -184,3 +184,27 @@ def test_attn_carried_sums_of_every_kind(D, hint):
         o, l, av, e = attn64(q[b], c.keys[b][part], c.values[b][part], D ** -0.5)
         within(out[b], o, (2 * e[:, None] + 2.0 ** -13) * av + HALF[BF16] * o.abs(), f"out {b}")
         within(lse[b], l, e + 2.0 ** -20 * (l.abs() + 1), f"lse {b}")
+
+
+@pytest.mark.parametrize("nats", [8, 12, 16, 18, 20])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D, n, group, columns", [(64, 16, 4, None), (128, 500, 1, None), (256, 700, 9, None),
+                                                  (64, 3000, 9, 100000), (128, 3000, 4, 100000), (256, 3000, 1, 100000)])
+def test_attn_keys_far_below_the_largest_score(nats, dtype, D, n, group, columns):
+    """A key whose score lies `nats` above the others' and whose value is 0: the output consists of the others alone.
+    Their weights are held to 2^-40 of the largest, each, in fp16; the rest of the tolerance is check_attn's."""
+    g = gen(nats)
+    c = Paged([n], 1, D, 16, dtype, seed=nats)
+    q = randn(g, 1, 1, D, dtype=dtype).expand(1, group, D).contiguous()
+    k, v = 0.05 * randn(g, n, 1, D, dtype=F32), 300 + 30 * randn(g, n, 1, D, dtype=F32)
+    one = q[0, 0].float()
+    k[n // 3] = one * (nats * D ** 0.5 / (one @ one))
+    v[n // 3] = 0
+    set_rows(c, 0, k=k.to(dtype), v=v.to(dtype))
+    if columns:
+        c = c.widened(columns)
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, output_lse=True)
+    o, l, av, e = attn64(q[0], c.keys[0], c.values[0], D ** -0.5)
+    held = 2.0 ** -40 * c.values[0][:, 0].double().abs().sum(0) if dtype == F16 else 0.0
+    within(out[0], o, 2 * (e[:, None] + 2.0 ** -15) * av + HALF[dtype] * o.abs() + TINY[dtype] + held, "out")
+    within(lse[0], l, e + 2.0 ** -20 * (l.abs() + 1), "lse")
