@@ -10,8 +10,10 @@
 //
 // The angle.  position * inv_freq has up to 55 significant bits; fp32 would leave an error of
 // position * 2^-24 radians.  It is formed in fp64 and reduced by k 2 pi with 2 pi in two parts, so the
-// reduced angle is good to about 1e-15 * k before its rounding to fp32 (2^-23 at most); the fast sine and
-// cosine are then within 2^-21.2 of the exact ones, below a sixteenth of fp16's rounding of a turned element.
+// reduced angle is good to about 1e-15 * k.  For 16-bit activations it is rounded to fp32 (2^-23 at most), and the fast
+// sine and cosine are then within 2^-21 of the exact ones, below a sixteenth of fp16's rounding of a turned element.  fp32
+// activations would lose three bits by that: theirs are good to 2^-24 (turn_fp32; 32768 tokens of 16 + 2 heads of 256 202 us
+// as with the fast ones, 100000 tokens of 1 + 1 heads of 64, which share no angles, 35 against 31; with sincos in fp64 42).
 //
 // Layout.  A lane holds 8 neighbouring columns, a row (one head of q, k or v) lies in D / 8 lanes of one
 // warp, and a lane keeps its columns for all rows of its token: its cosines and signed sines, eight of each,
@@ -44,6 +46,30 @@ __device__ __forceinline__ float2 turn(int position, float f, float mscale)
     const double k = rint(x * kInv);
     const float r = (float)fma(-k, kTwoPiLo, fma(-k, kTwoPiHi, x));
     return make_float2(__cosf(r) * mscale, __sinf(r) * mscale);
+}
+
+// The same to fp32's rounding.  The angle is reduced to |r| <= pi/4 by k quarters of a turn; with r = hi + lo in fp32 and
+// z = hi^2, the Taylor series sin r = hi + lo cos r + hi z (-1/3! + z/5! - ..), cos r = 1 - z/2 - hi lo + z^2 (1/4! - ..)
+// end at hi^9 and hi^10 (the next terms are below 2e-9), and what 1 - z/2 and z lose to their rounding is added again.
+__device__ __forceinline__ float2 turn_fp32(int position, float f, float mscale)
+{
+    constexpr double kQuarterHi = 1.5707963267948966, kQuarterLo = 6.123233995736766e-17, kInv = 0.6366197723675814;
+    constexpr double kWhole = 6755399441055744.0;  // 1.5 * 2^52: a sum with it is rounded to whole numbers
+    const double x = (double)position * (double)f, t = fma(x, kInv, kWhole), k = t - kWhole;
+    const int quarter = __double2loint(t);
+    const double r = fma(-k, kQuarterLo, fma(-k, kQuarterHi, x));
+    const float hi = (float)r, lo = (float)(r - (double)hi), z = hi * hi, z_lo = fmaf(hi, hi, -z);
+    float c = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+    c = fmaf(c, z, -1.f / 720.f);
+    c = fmaf(c, z, 1.f / 24.f);
+    const float half = 0.5f * z, near = 1.f - half;
+    c = near + (((1.f - near) - half) + fmaf(z * z, c, fmaf(-hi, lo, -0.5f * z_lo)));
+    float s = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(s, z, 1.f / 120.f);
+    s = fmaf(s, z, -1.f / 6.f);
+    s = hi + fmaf(hi * z, s, lo * c);
+    const float cq = quarter & 1 ? s : c, sq = quarter & 1 ? c : s;
+    return make_float2((quarter + 1 & 2 ? -cq : cq) * mscale, (quarter & 2 ? -sq : sq) * mscale);
 }
 
 // CTAs an SM that the registers are cut for: six where next to nothing is spilled for it
@@ -85,7 +111,9 @@ __global__ void __launch_bounds__(kRopeThreads, rope_ctas(sizeof(typename A::raw
     const int here = (int)min((long long)tokens, p.T - t0) * n;
     for (int i = threadIdx.x; i < here; i += kRopeThreads) {
         const int tt = i / n, j = i - tt * n;
-        angles[tt * pitch + j] = turn(p.positions[t0 + tt], p.inv_freq[j], p.mscale);
+        const int position = p.positions[t0 + tt];
+        const float f = p.inv_freq[j];
+        angles[tt * pitch + j] = sizeof(raw) == 4 ? turn_fp32(position, f, p.mscale) : turn(position, f, p.mscale);
     }
     __syncthreads();
 

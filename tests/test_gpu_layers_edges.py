@@ -12,7 +12,7 @@ import torch
 
 import gated_deltanet_linear_17_b200 as gdn
 from gated_deltanet_linear_17_b200 import _layers
-from test_gpu_layers import BF16, F16, F32, HALF, TINY, Paged, attn64, gen, norm64, randn, within
+from test_gpu_layers import BF16, F16, F32, HALF, TINY, Paged, attn64, gen, norm64, randn, rope64, within
 
 pytestmark = pytest.mark.gpu
 
@@ -53,6 +53,30 @@ def test_norm_of_two_sizes_from_two_threads(width, dtype):
     for (x, w, r), (out, _) in zip(ins, outs):
         _, y = norm64(x, w, r, None, 1e-6, 0.0)
         within(out, y, (HALF[dtype] + 2.0 ** -17) * y.abs(), "out")
+
+
+# ------------------------------------------------------------------ rope
+
+
+@pytest.mark.parametrize("farthest", [50, 1 << 16, (1 << 31) - 1])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("mscale", [1.0, 1.3])
+def test_rope_of_fp32_is_good_to_fp32(farthest, interleaved, mscale):
+    """A factor is within 2^-24 of the exact one, and its product with mscale is rounded; the two products of an element
+    are rounded once more each at most (relative: 2^-24 + 2^-24 + 2^-24 < 2^-22 of mscale (|a| + |b|)), and their sum.
+    Frequencies of every size, among them some whose angles lie beside whole quarters of a turn; either sign of the
+    position."""
+    g = gen(farthest % 91)
+    T, D = 3000, 128
+    q, k = randn(g, T, 2, D, dtype=F32), randn(g, T, 1, D, dtype=F32)
+    pos = torch.randint(-farthest, farthest, (T,), generator=g, device="cuda").to(torch.int32)
+    f, _ = gdn.rope_inv_freq(D)
+    f[::7] = math.pi / 2 ** torch.arange(10, device="cuda")
+    f[3::11] = 9.7 * torch.rand(6, generator=g, device="cuda")
+    got = gdn.rope_fwd(q, k, pos, f, interleaved=interleaved, mscale=mscale)
+    for x, y in zip((q, k), got):
+        want, size = rope64(x, pos, f, interleaved, mscale)
+        within(y, want, 2.0 ** -22 * size + 2.0 ** -24 * want.abs(), "turned")
 
 
 # ------------------------------------------------------------------ paged attention
