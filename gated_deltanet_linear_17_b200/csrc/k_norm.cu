@@ -49,6 +49,19 @@ __device__ __forceinline__ float rcp(float x)
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// max |y| / 448, at least kMinScale, and 1 / scale: a multiplication or an approximate reciprocal and one step of Newton, so
+// that each is rounded about once.  (Infinity has no such step.)  Then y (1 / scale) is within 2^-23 of y / scale; the
+// division itself, two operations an element, moved 2 % fewer bytes at rounding borders and took 2 to 4 % longer.
+__device__ __forceinline__ float scale_of_max(float m)
+{
+    const float c = 1.f / kE4m3Max, q = m * c, e = fmaf(-q, kE4m3Max, m);
+    return absmax_nan(kMinScale, m < INFINITY ? fmaf(e, c, q) : q);
+}
+__device__ __forceinline__ float inverse(float scale)
+{
+    const float r = rcp(scale), e = fmaf(-scale, r, 1.f);
+    return scale < INFINITY ? fmaf(r, e, r) : r;
+}
 // g / (1 + e^-g); e^-g = infinity gives -0, as the formula does
 __device__ __forceinline__ float2 silu(float2 g)
 {
@@ -433,7 +446,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 if (kShift) {
                     if (leads) group_max[mine_row][(t + k * L) / kGroupLanes] = m, group_lead[mine_row][(t + k * L) / kGroupLanes] = lead;
                 } else {
-                    const float scale = absmax_nan(kMinScale, m * (1.f / kE4m3Max)), inv = __fdividef(1.f, scale);
+                    const float scale = scale_of_max(m), inv = inverse(scale);
                     if (has(k)) {
 #pragma unroll
                         for (int j = 0; j < H; ++j) z[k][j] = fmul2(z[k][j], make_float2(inv, inv));
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
         if (kShift && quant == GDN_QUANT_BLOCK) {
             if (L > 32) __syncthreads();
             else __syncwarp();
+            // (two scales a unit, so without scale_of_max's second step: 16384 x 1537 fp32 with a gate 86 us, 89 with it)
             auto scale_of = [&](int g) {
                 return absmax_nan(kMinScale, absmax_nan(group_max[mine_row][g], group_lead[mine_row][g + 1]) * (1.f / kE4m3Max));
             };
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(norm_block(L), norm_ctas(L)) rms_norm_kernel(c
                 __syncthreads();
                 most = lanes_max<kWarps>(red[1][t & (kWarps - 1)]);
             }
-            const float scale = absmax_nan(kMinScale, most * (1.f / kE4m3Max)), inv = __fdividef(1.f, scale);
+            const float scale = scale_of_max(most), inv = inverse(scale);
             if (live && t == 0) p.scales[row] = scale;
 #pragma unroll
             for (int k = 0; k < NV; ++k) {

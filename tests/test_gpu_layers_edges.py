@@ -55,6 +55,21 @@ def test_norm_of_two_sizes_from_two_threads(width, dtype):
         within(out, y, (HALF[dtype] + 2.0 ** -17) * y.abs(), "out")
 
 
+@pytest.mark.parametrize("quant", ["row", "block"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("width", [128, 2048, 4096])
+def test_norm_scales_are_rounded_once(width, dtype, quant):
+    """Rows of one value in all places, weight and rstd 1: y is that value, and the scale is value / 448 rounded once.
+    eps = 1 - value^2 makes rstd the root of 1 up to the rounding of the mean of equal squares, which a power of two
+    as width leaves exact."""
+    x = torch.tensor([0.0625, 0.125, 0.25, 0.375, 0.5, 0.625, 0.75, 0.875], device="cuda")
+    for value in x.tolist():
+        rows = torch.full((5, width), value, device="cuda", dtype=dtype)
+        _, _, scales = gdn.rms_norm(rows, torch.ones(width, device="cuda", dtype=dtype), eps=1 - value * value, quant=quant)
+        want = torch.tensor(value, dtype=torch.float64) / 448
+        assert (scales == want.float().item()).all()
+
+
 # ------------------------------------------------------------------ rope
 
 
