@@ -260,10 +260,10 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     q [B, Hq, D] bf16 or fp16, D 64, 128 or 256; k_cache, v_cache [P, page_size, Hkv, D] of q's type, Hq a
     multiple of Hkv (query head h reads key/value head h // (Hq // Hkv)); block_table [B, max_pages]
     int32, the pages of each sequence in order (entries past its last page are not read); seq_lens [B]
-    int32, the keys of each sequence, the new token's own among them.  ``scale`` is positive (default
-    1/sqrt(D)).  ``max_seqlen`` is the longest
-    length if known, else 0 (it sets how the work is split).  A length of 0 gives a zero row and lse
-    -inf; a length beyond the table or a page outside the cache gives NaN for that sequence.
+    int32, the keys of each sequence, the new token's own among them.  ``scale`` is positive, in fp32's
+    range (default 1/sqrt(D)).  ``max_seqlen`` is the longest length if known, else 0 (it sets how the work
+    is split).  A length of 0 gives a zero row and lse -inf; a length beyond the table or a page outside the
+    cache gives NaN for that sequence.
     ``lse`` [B, Hq] fp32 is written when given or when ``output_lse``.  ``workspace``: a device buffer
     of ``paged_attn_workspace_bytes`` bytes, allocated here when not given; calls that can overlap on
     the GPU, replayed graphs among them, need buffers of their own."""
@@ -285,8 +285,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     max_seqlen = min(int(max_seqlen), 0x7fffffff)
     if max_seqlen < 0:
         raise ValueError("max_seqlen must not be negative")
-    if scale is not None and not 0.0 < scale < math.inf:
-        raise ValueError(f"scale must be positive and finite (got {scale})")
+    if scale is not None and not 1.4e-45 <= scale <= 2.3e38:
+        raise ValueError(f"scale must be positive and finite in fp32, at most 2.3e38 (got {scale})")
     max_pages = tshape[1]
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")

@@ -1,6 +1,7 @@
 // Host side of the layer operators (include/gdn_layers.h): argument checks and launches.
 #include "gdn_layers.h"
 
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -156,6 +157,8 @@ int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, 
     int rc = attn_sizes(B, Hq, Hkv, D, page_size, max_pages, max_seqlen, &max_len);
     if (rc) return rc;
     if (P < 0 || !dtype_ok(act_dtype)) return GDN_ERR_BAD_SHAPE;
+    const float log2e = 1.44269504f;
+    if (!(scale <= 0.f) && !(scale * log2e <= FLT_MAX)) return GDN_ERR_BAD_SHAPE;  // NaN among them
     if (act_dtype == GDN_DTYPE_FP32 || (int64_t)P * page_size >= (int64_t(1) << 31)) return GDN_ERR_UNSUPPORTED;
     if (B == 0) return GDN_OK;
     const bool keys = P > 0 && max_pages > 0;
@@ -184,7 +187,7 @@ int gdn_paged_attn_fwd(const void *q, const void *k_cache, const void *v_cache, 
     p.begun = static_cast<int4 *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(p.begun + plan.ctas);
     p.part = reinterpret_cast<float *>(p.part_ml + 32 * (size_t)plan.ctas);
-    p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * 1.44269504f;
+    p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * log2e;
     p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.group = Hq / Hkv, p.row_tiles = (Hq / Hkv + 15) / 16;
     p.P = P, p.page_size = page_size, p.max_pages = max_pages, p.ctas = plan.ctas, p.direct = plan.direct;
     p.capacity = (long long)page_size * max_pages;

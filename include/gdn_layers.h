@@ -133,7 +133,8 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  *                 not read
  *   seq_lens      int32 [B], 0 .. max_pages * page_size.  A length of 0 gives a
  *                 zero row and lse = -infinity
- *   scale         <= 0 selects 1/sqrt(D)
+ *   scale         <= 0 selects 1/sqrt(D); else up to 2.3e38 (NaN and infinity
+ *                 are GDN_ERR_BAD_SHAPE)
  *   out           [B, Hq, D] of act_dtype; lse fp32 [B, Hq] or NULL
  *   max_seqlen    the longest sequence if known, else 0: keeps the grid and the
  *                 workspace of a small call small; any value gives a right result

@@ -247,3 +247,25 @@ def test_attn_keys_far_below_the_largest_score(nats, dtype, D, n, group, columns
     held = 2.0 ** -40 * c.values[0][:, 0].double().abs().sum(0) if dtype == F16 else 0.0
     within(out[0], o, 2 * (e[:, None] + 2.0 ** -15) * av + HALF[dtype] * o.abs() + TINY[dtype] + held, "out")
     within(lse[0], l, e + 2.0 ** -20 * (l.abs() + 1), "lse")
+
+
+@pytest.mark.parametrize("scale", [1e-50, 1e-46, 5e38, 1e300, 2.4e38])
+def test_attn_refuses_scales_beyond_fp32(scale):
+    """1e-50 is positive and finite, but 0 in fp32, which stands for the default."""
+    c = Paged([30, 40], 2, 64, 16, BF16)
+    with pytest.raises(ValueError, match="scale"):
+        gdn.paged_attn_fwd(randn(gen(1), 2, 4, 64), c.k, c.v, c.table, c.seq_lens, scale=scale)
+
+
+@pytest.mark.parametrize("scale", [1.5e-45, 1e-30, 2e38])
+def test_attn_takes_scales_at_the_ends_of_fp32(scale):
+    """The smallest: all scores 0, out the mean of the values.  The largest: the largest score takes all (they differ
+    by far more than 2^-100 here)."""
+    c = Paged([300], 1, 64, 16, BF16, seed=2)
+    q = randn(gen(1), 1, 4, 64)
+    out, lse = gdn.paged_attn_fwd(q, c.k, c.v, c.table, c.seq_lens, scale=scale, output_lse=True)
+    s = torch.einsum("hd,nd->hn", q[0].double(), c.keys[0][:, 0].double())
+    v = c.values[0][:, 0].double()
+    want = v.mean(0).expand(4, 64) if scale < 1 else v[s.argmax(1)]
+    within(out[0], want, HALF[BF16] * want.abs() + 2.0 ** -14 * v.abs().mean(0), "out")
+    assert scale > 1 or (lse - math.log(300)).abs().max() < 2.0 ** -17
