@@ -46,6 +46,13 @@ def _layers_lib():
     return _lib
 
 
+_MOST = 0x7fffffff  # of the sizes that the library takes in 32 bits; ctypes would cut larger ones down
+
+
+def _too_large(*sizes):
+    return ValueError(f"a size of {max(sizes)} is beyond 2^31 - 1")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -116,6 +123,8 @@ def rms_norm(x, weight, residual=None, gate=None, eps=1e-6, weight_offset=0.0, q
         raise ValueError("x must be [..., width] with at least one column")
     act, shape = _act(x, "x"), x.shape
     width = shape[-1]
+    if width > _MOST:
+        raise _too_large(width)
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
     wdt = _f32 if _tensor(weight, "weight").dtype is _f32 else act
@@ -207,6 +216,8 @@ def rope_fwd(q, k, positions, inv_freq, v=None, k_cache=None, v_cache=None, slot
     act = _act(q, "q")
     T, Hq, D = q.shape
     Hkv = k.shape[1]
+    if Hq > _MOST or Hkv > _MOST or D > _MOST:
+        raise _too_large(Hq, Hkv, D)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _need(k, "k", act, (T, Hkv, D), dev)
@@ -288,6 +299,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, scale=None, max_s
     if scale is not None and not 1.4e-45 <= scale <= 2.3e38:
         raise ValueError(f"scale must be positive and finite in fp32, at most 2.3e38 (got {scale})")
     max_pages = tshape[1]
+    if B > _MOST or Hq > _MOST or D > _MOST or P > _MOST or page > _MOST or max_pages > _MOST:
+        raise _too_large(B, Hq, D, P, page, max_pages)
     if not q.is_contiguous():
         raise ValueError("q must be contiguous")
     _need(k_cache, "k_cache", act, (P, page, Hkv, D), dev)

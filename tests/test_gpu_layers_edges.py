@@ -269,3 +269,16 @@ def test_attn_takes_scales_at_the_ends_of_fp32(scale):
     want = v.mean(0).expand(4, 64) if scale < 1 else v[s.argmax(1)]
     within(out[0], want, HALF[BF16] * want.abs() + 2.0 ** -14 * v.abs().mean(0), "out")
     assert scale > 1 or (lse - math.log(300)).abs().max() < 2.0 ** -17
+
+
+def test_sizes_beyond_32_bits_are_refused():
+    """A width, head dimension or page count of 2^32 and something (8.6 GB of elements) is no smaller one."""
+    n = (1 << 32) + 64
+    x = torch.empty(n, device="cuda", dtype=BF16)
+    few = torch.zeros(1, device="cuda", dtype=torch.int32)
+    for call in (lambda: gdn.rms_norm(x, x), lambda: gdn.rms_norm(x, x, quant="block"),
+                 lambda: gdn.rope_fwd(x.view(1, 1, n), x.view(1, 1, n), few, torch.ones(1, device="cuda")),
+                 lambda: gdn.rope_fwd(x.view(1, n // 64, 64), x.view(1, n // 64, 64), few, torch.ones(1, device="cuda")),
+                 lambda: gdn.paged_attn_fwd(x.view(1, 1, n), x.view(1, 1, 1, n), x.view(1, 1, 1, n), few.view(1, 1), few)):
+        with pytest.raises((ValueError, RuntimeError)):
+            call()
