@@ -77,8 +77,14 @@ def _on(index, stream):
         yield
 
 
-# the current device, and the current stream's handle on a device: each a tenth of what torch.cuda's own take
-_current_device, _current_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+def _stream_handle(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# The current device, and the current stream's handle on a device.  torch's private ones take a tenth of the public
+# ones' time; a torch without them (built for the CPU alone, or of another version) has the public ones.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _stream_handle)
 
 
 def _tensor(t, name):

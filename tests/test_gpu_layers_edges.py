@@ -282,3 +282,20 @@ def test_sizes_beyond_32_bits_are_refused():
                  lambda: gdn.paged_attn_fwd(x.view(1, 1, n), x.view(1, 1, 1, n), x.view(1, 1, 1, n), few.view(1, 1), few)):
         with pytest.raises((ValueError, RuntimeError)):
             call()
+
+
+def test_calls_by_torch_s_public_functions(monkeypatch):
+    """The device and the stream that a call runs on, where torch has no private functions for them."""
+    g = gen(5)
+    x, w = randn(g, 300, 256), randn(g, 256)
+    want = gdn.rms_norm(x, w)[0]
+    monkeypatch.setattr(_layers, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(_layers, "_current_stream", _layers._stream_handle)
+    assert torch.equal(gdn.rms_norm(x, w)[0], want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        assert _layers._current_stream(0) == side.cuda_stream
+        got = gdn.rms_norm(x, w)[0]
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)

@@ -2,10 +2,16 @@
 torch (CPU only: no call here enqueues work)."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import pytest
 
 from gated_deltanet_linear_17_b200 import _binding as B
 from test_layers_abi import _attn, lib  # noqa: F401 (a fixture)
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.mark.parametrize("scale", [float("nan"), float("inf"), 3e38, 2.4e38])
@@ -18,3 +24,25 @@ def test_attn_refuses_a_scale_that_is_no_number(lib, scale):  # noqa: F811
 @pytest.mark.parametrize("scale", [0.0, -1.0, float("-inf"), 1e-45, 2.3e38])
 def test_attn_takes_other_scales(lib, scale):  # noqa: F811
     assert _attn(lib, scale=scale, B=0) == B.GDN_OK
+
+
+def test_package_imports_without_torch_s_private_functions():
+    """A torch that has renamed them, or is built without CUDA, still imports the package; the public ones serve."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+import gated_deltanet_linear_17_b200 as gdn
+from gated_deltanet_linear_17_b200 import _layers
+assert _layers._current_device is torch.cuda.current_device
+assert _layers._current_stream is _layers._stream_handle
+try:
+    gdn.rms_norm(torch.zeros(2, 8), torch.zeros(8))
+except RuntimeError as e:
+    assert "CUDA device" in str(e)
+else:
+    raise SystemExit("a host tensor was taken")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=600)
+    assert r.returncode == 0, r.stderr
