@@ -196,6 +196,8 @@ def rope_inv_freq(rotary, base=10000.0, scaling=None, factor=1.0, original_max=4
 
         low, high = max(math.floor(place(beta_fast)), 0), min(math.ceil(place(beta_slow)), rotary - 1)
         ramp = ((i / 2 - low) / max(high - low, 1e-3)).clamp(0.0, 1.0)
+        if place(beta_slow) <= 0.0:  # no angle turns more often than that: the ramp ends before the first
+            ramp = torch.ones_like(i)
         f = f * (1.0 - ramp) + f / factor * ramp
         mscale = 0.1 * math.log(factor) + 1.0
     return f.float().to(device), mscale

@@ -2,12 +2,15 @@
 torch (CPU only: no call here enqueues work)."""
 from __future__ import annotations
 
+import math
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
+import gated_deltanet_linear_17_b200 as gdn
 from gated_deltanet_linear_17_b200 import _binding as B
 from test_layers_abi import _attn, lib  # noqa: F401 (a fixture)
 
@@ -46,3 +49,17 @@ else:
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT, timeout=600)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("original_max", [1, 4, 6, 7, 40, 4096, 1 << 20])
+@pytest.mark.parametrize("rotary", [2, 8, 64, 128])
+def test_yarn_divides_every_slow_angle(original_max, rotary):
+    """An angle that turns at most beta_slow times over original_max positions is divided by the factor, the first too;
+    one that turns at least beta_fast times is kept; the others lie between."""
+    plain, _ = gdn.rope_inv_freq(rotary, device="cpu")
+    yarn, _ = gdn.rope_inv_freq(rotary, scaling="yarn", factor=8.0, original_max=original_max, device="cpu")
+    turns = original_max * 10000.0 ** (-torch.arange(0, rotary, 2, dtype=torch.float64) / rotary) / (2 * math.pi)
+    ratio = yarn.double() / plain.double()
+    assert torch.allclose(ratio[turns <= 1.0], torch.tensor(0.125, dtype=torch.float64), rtol=2.0 ** -22)
+    assert torch.allclose(ratio[turns >= 32.0], torch.tensor(1.0, dtype=torch.float64), rtol=2.0 ** -22)
+    assert ((ratio >= 0.125 - 1e-6) & (ratio <= 1 + 1e-6)).all()
