@@ -2,8 +2,8 @@
 //
 //   s_j = scale q . k_j,  out = sum_j e^{s_j} v_j / sum_j e^{s_j},  lse = log sum_j e^{s_j}
 //
-// Every key and value is read once from HBM and used by the G = Hq / Hkv query heads of its head:
-// G flops a byte of a 16-bit cache, so up to G of about 250 the cache's bytes bound it, and the matrix
+// Every key and value is read from HBM once for each 16 of the G = Hq / Hkv query heads of its head (once up to G = 16,
+// twice from 17 on): up to 16 flops a byte of a 16-bit cache, so the cache's bytes bound it, and the matrix
 // products only have to keep up: mma.sync, which takes its operands from any shared-memory tile and leaves
 // the softmax its scores in registers; one octet of query rows costs a sixth of the SM's time.
 //
@@ -32,16 +32,16 @@
 // as large as the output's own rounding into it, and the second product costs nothing beside the memory traffic.  In bf16
 // the pair holds 16 bits or more of p, whatever its size.  fp16 ends at 2^-24, so there every weight is 2^15 p (kRaise; up
 // to 32768), and the pair is good to 22 bits or 2^-25, which is 2^-40 of the largest weight: 16 bits of a key that lies 16.6
-// nats below the largest score, 11 bits at 20.  The sum of exponentials
-// takes them unrounded, so lse is good to fp32.  The tensor core cuts off what an addition to its accumulator drops
+// nats below the largest score, 11 bits at 20.  The sum of exponentials takes them unrounded, so lse is good to fp32.  The
+// tensor core cuts off what an addition to its accumulator drops
 // (up to 2^-23 of the accumulator, always towards zero), so no more than 512 additions (256 tiles of 16 keys) go to one: a
 // piece of the list ends after kMostKeys keys, and the CTA adds its pieces of a pair up in fp32, rounded; a cluster's CTA that
 // gets more keys than its hint said sums a tile's products on their own and adds them so.  (300 rows over 131072 keys of
 // positive values, D = 256: on average 8e-5 too small, without that 3.2e-4; over 10^6 keys, D = 128, 4e-5 against 1.5e-3.)
 //
-// Measured (bf16): 256 sequences of 1024 to 16384 keys, 16 / 2 heads of 256: 692 us, 6.8 TB/s (a read-only stream
+// Measured (bf16): 256 sequences of 1024 to 16384 keys, 16 / 2 heads of 256: 698 us, 6.75 TB/s (a read-only stream
 // passes the copy rate); 64 of 1 to 8192 keys, 32 / 8 heads of 128: 172 us, 6.4 TB/s; one of 131072 keys, 16 / 2
-// heads of 256: 52 us, 5.2 TB/s, 8 us of them the start, the CTAs' uneven end and the join; one of 700 keys: 7 us.
+// heads of 256: 52 us, 5.2 TB/s, 8 us of them the start, the CTAs' uneven end and the join; one of 700 keys: 7.5 us.
 #include <algorithm>
 
 #include "gdn_layers.h"
@@ -686,9 +686,10 @@ __global__ void __launch_bounds__(Shape<D, NT, DIRECT>::kThreads, Shape<D, NT, D
 // Joins the pieces of every pair that a CTA of the first kernel began and did not finish: piece 0 lies in
 // that CTA's place 1, piece j in place 0 of the j-th CTA after it.  Every CTA reads the list of such pairs;
 // a query head of a pair of few pieces is one warp's work, of many pieces (a long sequence cut over the whole
-// GPU) one CTA's for each 32 columns, its threads spread over the pieces.  Its CTAs are small enough (8K registers,
-// 13 KB) to lie beside the first kernel's on every SM before that ends; what is left behind its end is then two
-// loads, one waiting for the other.
+// GPU) one CTA's for each 32 columns, its threads spread over the pieces.  Where a CTA (8K registers, 8 KB) finds room
+// beside the first kernel's two on an SM, it lies there before that ends, and what is left behind its end is two
+// loads, one waiting for the other: at D = 256, and at D = 64 with up to 8 query heads.  The others' registers (D = 128:
+// 59K of 64K and more) let it in as their CTAs leave.
 constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32, kJoinCtas = 4 * kAttnSms, kFewPieces = 4;
 
 template <int D, bool F16>
@@ -701,7 +702,9 @@ __global__ void __launch_bounds__(kJoinThreads, 8) paged_attn_join_kernel(const 
     __shared__ uint32_t upto[kAttnMaxCtas], warp_total[kJoinWarps];  // many << 16 | few: items up to and with this one
     __shared__ float4 part[kGroups][kCols];
     __shared__ float2 part_ml[kGroups];
-    constexpr int kInFlight = 5;  // pieces that a thread reads at a time: 296 CTAs cut two pairs into 148 pieces, 9.25 a thread
+    // pieces that a thread reads at a time (131072 keys cut by 296 CTAs, 3, 5 and 8 at a time: one head of 256, 18.5 pieces a
+    // thread, 35.9, 34.2, 35.2 us; two, 9.25, 53.1, 52.0, 53.0; four of 128, 4.6, 50.8, 50.5, 51.4; eight, 2.3, 88.7, 88.8, 89.8)
+    constexpr int kInFlight = 5;
     begin_early();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t items[kPer], mine = 0;

@@ -66,8 +66,9 @@ extern "C" {
  *   rows          >= 0 (0 is a no-op); width 1 .. GDN_NORM_MAX_WIDTH, at most
  *                 GDN_NORM_MAX_WIDTH - 8 where it is no multiple of 8
  * A row that holds a NaN or an infinity in z comes out as NaN where the formula
- * gives NaN.  |z| from about 1.8e19 on overflows the fp32 mean and the row
- * comes out as zero.
+ * gives NaN.  Where the sum of a row's z^2 is beyond fp32 (3.4e38: |z| of 1.8e19,
+ * or of 1e17 in each of 32768 columns) the row comes out as zero.  Below a gate
+ * of -87 the factor gate / (1 + e^-gate), under 2e-36, is zero.
  * Alignment: 16 bytes for the matrices and weight, 4 for scales.  Errors:
  * GDN_ERR_NULL_ARG, GDN_ERR_BAD_SHAPE (sizes, unknown codes), GDN_ERR_UNSUPPORTED
  * (width, rows > 2^31 - 32), GDN_ERR_ALIGNMENT, GDN_ERR_OVERLAP (an output on an
@@ -121,7 +122,8 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  *
  *     s_j = scale q . k_j,  p = softmax(s),  out = sum_j p_j v_j,  lse = log sum_j e^s_j
  * over the seq_lens[b] keys of sequence b, the new token's own among them (it
- * is written first, see gdn_rope_fwd).  Query head h reads key/value head
+ * is written first, see gdn_rope_fwd).  The cache is read once for each 16 query
+ * heads of a key/value head.  Query head h reads key/value head
  * h / (Hq / Hkv).  Token j of sequence b lies on page block_table[b][j /
  * page_size], at place j % page_size.  Several new tokens of one sequence
  * (speculative decoding) are as many rows with the same pages and growing
@@ -146,7 +148,9 @@ int gdn_rope_fwd(const void *q, const void *k, const void *v, const int32_t *pos
  * A sequence with a length outside its range or a page outside [0, P) among its
  * pages reads nothing out of bounds and comes out as NaN (out and lse), the
  * others are not affected.  NaN and infinities in a sequence's own rows come out
- * as NaN where the formula gives NaN, an infinity in v as an infinity or NaN (p is
+ * as NaN where the formula gives NaN, but for a sequence whose every score is
+ * -infinity: it comes out as one without keys (a zero row, lse = -infinity).  An
+ * infinity in v comes out as an infinity or NaN (p is
  * multiplied in two parts, the second of either sign); cache rows that no sequence lists are never read.
  * A key's weight is held to 16 bits or more, in fp16 of keys more than 16 nats below the row's largest score to 2^-40 of
  * the largest weight.

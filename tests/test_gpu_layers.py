@@ -2,14 +2,15 @@
 the write into a paged cache, the attention of one new token over it, and one decode step of all.
 
 Tolerances, per element, from the arithmetic (u = 2^-24 is the fp32 unit roundoff):
-  norm       y is a product of five fp32 factors.  The sum of squares of up to 32768 columns is 64
-             sequential fused additions a lane and a tree of at most 20, all terms positive: 84 u, half of
-             it in the root.  __expf(-g) is within (2 + 1.2 |g|) 2 u, |g| < 8 in the tests: 24 u.  With the
-             products, the division and the root: below 100 u < 2^-17, relative, plus the output's own
-             rounding.  In 8 bits: half a step of e4m3, 2^-4 relative or 2^-10 below its normal range, in
-             units of the scale.
-  rope       the reduced angle is rounded to fp32 (|th| <= pi: 2^-23), sin and cos are within 2 ulp
-             (2^-23), then two products and a sum: below 2^-20 mscale (|a| + |b|), plus the output's rounding.
+  norm       y is a product of four fp32 factors.  The sum of squares of up to 32768 columns is 32
+             sequential fused additions a lane at most and a tree of at most 20, all terms positive: 52 u, half
+             of it in the root.  e^-g is 2^(-g log2 e): its argument is off by 2 u, relative, which is 2 |g| u of
+             it, |g| < 8 in the tests, and the approximate exponential and reciprocal by 4 u each: 24 u.  With the
+             products and the root: below 100 u < 2^-17, relative, plus the output's own rounding.  In 8 bits:
+             half a step of e4m3, 2^-4 relative or 2^-10 below its normal range, in units of the scale.
+  rope       the reduced angle is rounded to fp32 (|th| <= pi: 2^-23), the fast sine and cosine are within 2^-21.2
+             (fp32 activations: 2^-24, both roundings in it), then two products and a sum: below
+             2^-20 mscale (|a| + |b|), plus the output's rounding.
   attention  a score is a sum of D exact products accumulated in fp32 on the tensor core, in D / 16 steps
              whose inner additions may be cut off rather than rounded (2^-22 of the magnitudes each), scaled:
              e = (D / 16 + 4) 2^-22 scale sum |q k|.  A probability is then off by e + 2^-21 (exp2) + 2^-16
